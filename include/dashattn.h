@@ -60,7 +60,8 @@ typedef enum {
   DASH_ERR_UNSUPPORTED = 2,
   DASH_ERR_WORKSPACE_TOO_SMALL = 3,
   DASH_ERR_CUDA = 4,
-  DASH_ERR_DEVICE_TIMEOUT = 5
+  DASH_ERR_DEVICE_TIMEOUT = 5,
+  DASH_ERR_OUT_OF_PAGES = 6 /* dash_attn_pages_grow: too few free pages */
 } dash_status_t;
 
 typedef enum { DASH_F32 = 0, DASH_F16 = 1, DASH_BF16 = 2 } dash_dtype_t;
@@ -424,6 +425,164 @@ dash_status_t dash_attn_sparse_mask(const dash_tensor_t* q, const dash_tensor_t*
                                     const dash_options_t* opts, dash_stream_t stream);
 
 /*
+ * Dense and sliding-window attention: the layers that a model keeps beside
+ * the sparse ones, on the same tensors and caches.  Row i sees key j when
+ *   j <= i  and  (window == 0  or  j > i - window  or  j < sinks),
+ * i.e. itself, the window - 1 tokens before it and the first `sinks` tokens;
+ * window == 0 is plain causal attention (sinks then adds nothing):
+ *   out_i = sum_j p_ij v_j,  p_ij = exp(q_i . k_j / sqrt(d) - lse_i).
+ *   window   0 or more; sinks  0 .. 128.
+ *   seqlens  device int32 [B] or NULL: only the first seqlens[b] tokens of
+ *            sequence b are there (0 .. S).  Rows from seqlens[b] on get
+ *            out = 0 and lse = -inf, zero gradients, and whatever their q, k,
+ *            v and dout hold (NaN too) reaches no other row.  A value out of
+ *            range is clamped and reported in the workspace status word.
+ *            The tokens before seqlens[b] must be finite.
+ *   lse      device fp32 [B, H, S]: natural log-sum-exp of the row's visible
+ *            logits; NULL in the forward if not wanted.  The backward reads
+ *            the forward's.
+ * Strides of 0 over an extent above 1 are refused (DASH_ERR_UNSUPPORTED).
+ */
+
+/* Bytes of workspace of dash_attn_window_fwd (a status word). 0: rejected arguments. */
+size_t dash_attn_window_fwd_workspace_size(const dash_tensor_t* q, const dash_tensor_t* k);
+
+/*
+ * Forward over q [B, S, H, d], k, v [B, S, Hkv, d] -> out [B, S, H, d], every
+ * element written.  f16/bf16: tensor cores, P rounded to the input type for
+ * the second product; f32: CUDA cores throughout.
+ *   workspace  dash_attn_window_fwd_workspace_size() bytes, 256-byte aligned.
+ */
+dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
+                                   const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, dash_stream_t stream);
+
+/*
+ * Backward: the gradients of sum(dout * out) with respect to q, k and v, in
+ * the inputs' type (f32, f16 or bf16), every element written:
+ *   dS_ij = p_ij (dout_i . v_j - dout_i . out_i);  dq_i = sum_j dS_ij k_j / sqrt(d);
+ *   dk_j = sum_i dS_ij q_i / sqrt(d);  dv_j = sum_i p_ij dout_i
+ * (dk and dv summed over the heads of the group).  No atomics: the same
+ * result every time.
+ *   out, lse   the forward's, with the same q, k, v, seqlens, window, sinks.
+ *   workspace  dash_attn_window_bwd_workspace_size() bytes, 256-byte aligned.
+ */
+size_t dash_attn_window_bwd_workspace_size(const dash_tensor_t* q, const dash_tensor_t* k, int64_t window,
+                                           int64_t sinks);
+dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
+                                   const dash_tensor_t* out, const float* lse, const dash_tensor_t* dout,
+                                   const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* dq,
+                                   dash_tensor_t* dk, dash_tensor_t* dv, void* workspace, size_t workspace_bytes,
+                                   dash_stream_t stream);
+
+/*
+ * The same attention for one new token per sequence over its cache: the
+ * query of sequence b stands at position seqlens[b] - 1 (its own K and V are
+ * in the cache already).
+ *   q, out     [B, 1, H, d]; f16 or bf16.
+ *   kcache, vcache  [B, Lmax, Hkv, d]; or pages and a block table as for
+ *              dash_attn_decode_paged (page size 64 or 128).
+ *   seqlens    device int32 [B], 0 .. Lmax (max_blocks * page size); a
+ *              sequence of length 0 gets out = 0, lse = -inf.  A value out of
+ *              range is clamped and reported.
+ *   block_table  entries of pages that hold no visible token are not read.  A
+ *              page number outside the pool is reported
+ *              (DASH_ERR_INVALID_ARGUMENT in the status word); its tokens are
+ *              read as zeros.
+ *   lse        device fp32 [B, H] or NULL.
+ *   workspace  dash_attn_window_decode_workspace_size() bytes, 256-byte
+ *              aligned; it depends on the current device, not on B or Lmax.
+ * Cache values at tokens that are not visible are never used.  The result
+ * does not depend on timing.  The call can be captured into a graph; the work
+ * is split on the device by the lengths that seqlens holds when it runs.
+ */
+size_t dash_attn_window_decode_workspace_size(int64_t heads, int64_t kv_heads, int64_t head_dim);
+dash_status_t dash_attn_window_decode(const dash_tensor_t* q, const dash_tensor_t* kcache, const dash_tensor_t* vcache,
+                                      const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* out,
+                                      float* lse, void* workspace, size_t workspace_bytes, dash_stream_t stream);
+dash_status_t dash_attn_window_decode_paged(const dash_tensor_t* q, const dash_tensor_t* k_pages,
+                                            const dash_tensor_t* v_pages, const int32_t* block_table,
+                                            int64_t max_blocks, const int32_t* seqlens, int64_t window, int64_t sinks,
+                                            dash_tensor_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                            dash_stream_t stream);
+
+/*
+ * Pages of a paged cache.  The state is three device arrays:
+ *   block_table  int32 [batch, max_blocks]: sequence b holds the pages in the
+ *                first ceil(seqlens[b] / block) entries of its row; the other
+ *                entries are not read.
+ *   seqlens      int32 [batch].
+ *   refs         int32 [n_pages]: how many table entries hold each page
+ *                (entries of other tables or owners may be counted too); a
+ *                page is free when this is 0.
+ * One table serves the pools of all layers.  The calls only touch this state;
+ * dash_attn_pages_copy moves the pages' contents.  New pages are the lowest
+ * free ones, so every call is a function of the state.  Each call is one
+ * launch and can be captured into a graph.  What the state does not allow (a
+ * sequence out of range, the same destination twice, a length out of range)
+ * is found on the device before the first write: the call changes nothing
+ * and the workspace status word reads DASH_ERR_INVALID_ARGUMENT.  block is
+ * 64 or 128; at most 8192 sequences, batch * max_blocks and n_pages below 2^30.
+ *   workspace  dash_attn_pages_workspace_size() bytes, 256-byte aligned.
+ */
+size_t dash_attn_pages_workspace_size(int64_t batch, int64_t max_blocks, int64_t n_pages);
+
+/*
+ * Sequence dst[i] becomes a copy of sequence src[i] as both were before the
+ * call (i < n, device int32; dst without repeats; a row may be source and
+ * destination, as in reordering beams).  Pages are shared, not copied: refs
+ * of the source's pages go up, those of the pages that dst held go down.
+ * Entries that dst held beyond its new blocks become -1.
+ */
+dash_status_t dash_attn_pages_fork(int32_t* block_table, int64_t batch, int64_t max_blocks, int32_t* seqlens,
+                                   int32_t* refs, int64_t n_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                                   int block, void* workspace, size_t workspace_bytes, dash_stream_t stream);
+
+/* The sequences slots[i] (i < n, device int32, without repeats) give back their pages: length 0, entries -1. */
+dash_status_t dash_attn_pages_free(int32_t* block_table, int64_t batch, int64_t max_blocks, int32_t* seqlens,
+                                   int32_t* refs, int64_t n_pages, const int32_t* slots, int64_t n, int block,
+                                   void* workspace, size_t workspace_bytes, dash_stream_t stream);
+
+/*
+ * Room for n_new[b] >= 0 more tokens of every sequence (device int32 [batch];
+ * in order of b): where tokens will be written into a last page that other
+ * sequences share, the sequence gets a page of its own in its place and
+ * copy_src[b], copy_dst[b] (device int32 [batch]) name the copy to make, -1
+ * otherwise (the last holder of a page keeps it); then the pages that the new
+ * tokens need, and seqlens[b] += n_new[b].  With fewer free pages than that,
+ * nothing changes and the status word reads DASH_ERR_OUT_OF_PAGES.
+ */
+dash_status_t dash_attn_pages_grow(int32_t* block_table, int64_t batch, int64_t max_blocks, int32_t* seqlens,
+                                   int32_t* refs, int64_t n_pages, const int32_t* n_new, int block, int32_t* copy_src,
+                                   int32_t* copy_dst, void* workspace, size_t workspace_bytes, dash_stream_t stream);
+
+/*
+ * Pages to the low end of the pool: with `held` pages in use, the i-th used
+ * page at or past `held` moves to the i-th free one below it.
+ *   table_out, refs_out  the state after it (may be the inputs themselves);
+ *                entries past a sequence's blocks are copied as they are.
+ *   move_src, move_dst   device int32 [n_pages / 2]: the moves to make with
+ *                dash_attn_pages_copy, -1 past their number.
+ *   info         device int32 [2]: {number of moves, held}.
+ */
+dash_status_t dash_attn_pages_compact(const int32_t* block_table, int64_t batch, int64_t max_blocks,
+                                      const int32_t* seqlens, const int32_t* refs, int64_t n_pages, int block,
+                                      int32_t* table_out, int32_t* refs_out, int32_t* move_src, int32_t* move_dst,
+                                      int32_t* info, void* workspace, size_t workspace_bytes, dash_stream_t stream);
+
+/*
+ * Page src[i] of every pool to page dst[i] (i < n, device int32).  Entries
+ * below 0 or outside the pool are skipped.  No dst may be a src or a dst of
+ * another entry (the lists of dash_attn_pages_grow and _compact are so).
+ *   pools  n_pools host descriptors [n_pages, s, h, d] of one shape beyond
+ *          the first dimension, and one dtype (K and V of every layer; the
+ *          summaries [B, Hkv, t_cap, d] of sparse layers are a pool whose
+ *          pages are the sequences).
+ */
+dash_status_t dash_attn_pages_copy(const dash_tensor_t* pools, int64_t n_pools, const int32_t* src,
+                                   const int32_t* dst, int64_t n, dash_stream_t stream);
+
+/*
  * dash_attn_decode without a workspace argument.  The paper has no
  * counterpart: this serves callers that may not allocate device memory
  * while they run -- code inside another engine's execution hook (a serving
@@ -482,7 +641,8 @@ dash_status_t dash_attn_debug_sparse_stalled(const dash_tensor_t* q, const dash_
 /*
  * Synchronises `stream`, then reads the device status word of a workspace
  * last used by dash_attn_fwd / dash_attn_decode / dash_attn_sparse /
- * dash_attn_route / dash_attn_bwd (each call clears it when it starts).  Returns DASH_OK,
+ * dash_attn_route / dash_attn_bwd / dash_attn_window_* / dash_attn_pages_*
+ * (each call clears it).  Returns DASH_OK, DASH_ERR_OUT_OF_PAGES,
  * DASH_ERR_DEVICE_TIMEOUT (a bounded device wait expired; outputs of that
  * call are not valid), DASH_ERR_INVALID_ARGUMENT (a device-side value such
  * as seqlens[b] was out of range; it was clamped) or DASH_ERR_CUDA.

@@ -12,6 +12,7 @@ q, out [B, S, H, d]; k, v [B, S, Hkv, d]; summaries [B, Hkv, T, d] fp32.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -27,6 +28,7 @@ _STATUS = {
     3: "DASH_ERR_WORKSPACE_TOO_SMALL",
     4: "DASH_ERR_CUDA",
     5: "DASH_ERR_DEVICE_TIMEOUT",
+    6: "DASH_ERR_OUT_OF_PAGES",
 }
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
@@ -65,6 +67,19 @@ EXPORTED = (
     "dash_attn_decode_noalloc_status",
     "dash_attn_bwd_workspace_size",
     "dash_attn_bwd",
+    "dash_attn_window_fwd_workspace_size",
+    "dash_attn_window_fwd",
+    "dash_attn_window_bwd_workspace_size",
+    "dash_attn_window_bwd",
+    "dash_attn_window_decode_workspace_size",
+    "dash_attn_window_decode",
+    "dash_attn_window_decode_paged",
+    "dash_attn_pages_workspace_size",
+    "dash_attn_pages_fork",
+    "dash_attn_pages_free",
+    "dash_attn_pages_grow",
+    "dash_attn_pages_compact",
+    "dash_attn_pages_copy",
 )
 
 
@@ -136,6 +151,19 @@ def _load() -> ctypes.CDLL:
         "dash_attn_decode_noalloc_status": (i32, [vp]),
         "dash_attn_bwd_workspace_size": (sz, [T, T, i32]),
         "dash_attn_bwd": (i32, [T, T, T, vp, T, T, f32, i32, i32, O, T, T, T, vp, vp, sz, vp]),
+        "dash_attn_window_fwd_workspace_size": (sz, [T, T]),
+        "dash_attn_window_fwd": (i32, [T, T, T, vp, i64, i64, T, vp, vp, sz, vp]),
+        "dash_attn_window_bwd_workspace_size": (sz, [T, T, i64, i64]),
+        "dash_attn_window_bwd": (i32, [T, T, T, T, vp, T, vp, i64, i64, T, T, T, vp, sz, vp]),
+        "dash_attn_window_decode_workspace_size": (sz, [i64, i64, i64]),
+        "dash_attn_window_decode": (i32, [T, T, T, vp, i64, i64, T, vp, vp, sz, vp]),
+        "dash_attn_window_decode_paged": (i32, [T, T, T, vp, i64, vp, i64, i64, T, vp, vp, sz, vp]),
+        "dash_attn_pages_workspace_size": (sz, [i64, i64, i64]),
+        "dash_attn_pages_fork": (i32, [vp, i64, i64, vp, vp, i64, vp, vp, i64, i32, vp, sz, vp]),
+        "dash_attn_pages_free": (i32, [vp, i64, i64, vp, vp, i64, vp, i64, i32, vp, sz, vp]),
+        "dash_attn_pages_grow": (i32, [vp, i64, i64, vp, vp, i64, vp, i32, vp, vp, vp, sz, vp]),
+        "dash_attn_pages_compact": (i32, [vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "dash_attn_pages_copy": (i32, [T, i64, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -626,3 +654,241 @@ def decode_paged(q, k_pages, v_pages, block_table, seqlens, summaries, alpha: fl
                                        ctypes.byref(od), ws.data_ptr(), ws.numel(), _options(sigma, None),
                                        _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ dense / sliding-window attention
+
+
+@contextlib.contextmanager
+def _on(first: torch.Tensor, stream, *others):
+    """Device and stream of a call: every tensor on one device, buffers allocated for the stream they are used on."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be CUDA device tensors")
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream().cuda_stream
+    else:
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            yield torch.cuda.current_stream().cuda_stream
+
+
+def _array(t: torch.Tensor | None, name: str, shape, dtype=torch.int32):
+    """Device pointer of a contiguous array of the given shape (None: not given)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _scratch(nbytes: int, what: str, device, given: torch.Tensor | None) -> torch.Tensor:
+    if nbytes == 0:
+        raise DashError(1, f"arguments rejected by {what}: {_lib.dash_attn_last_error().decode()}")
+    if given is not None and not given.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return _workspace(nbytes, device, given)
+
+
+def window_fwd_workspace_size(q: torch.Tensor, k: torch.Tensor) -> int:
+    return _lib.dash_attn_window_fwd_workspace_size(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)))
+
+
+def window_fwd(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None, out=None,
+               return_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Causal attention over a sliding window and the first ``sinks`` tokens (see dash_attn_window_fwd).
+
+    window 0: every earlier token.  seqlens: optional int32 [B], the valid tokens of each sequence of a padded
+    batch.  Returns out [B, S, H, d], and with ``return_lse`` the log-sum-exp [B, H, S] fp32 too.
+    """
+    with _on(q, stream, k, v, seqlens, out, lse, workspace) as s:
+        qd, kd, vd = _desc(q), _desc(k), _desc(v)
+        B, S, H, _ = q.shape
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        if return_lse and lse is None:
+            lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
+        lp = _array(lse, "lse", (B, H, S), torch.float32)
+        ws = _scratch(_lib.dash_attn_window_fwd_workspace_size(ctypes.byref(qd), ctypes.byref(kd)),
+                      "dash_attn_window_fwd_workspace_size", q.device, workspace)
+        _check(_lib.dash_attn_window_fwd(ctypes.byref(qd), ctypes.byref(kd), ctypes.byref(vd),
+                                         _array(seqlens, "seqlens", (B,)), window, sinks, ctypes.byref(_desc(out)),
+                                         lp, ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    return (out, lse) if return_lse else out
+
+
+def window_bwd_workspace_size(q: torch.Tensor, k: torch.Tensor, window: int = 0, sinks: int = 0) -> int:
+    return _lib.dash_attn_window_bwd_workspace_size(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), window, sinks)
+
+
+def window_bwd(q, k, v, out, lse, dout, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None,
+               grads=None, workspace=None, stream=None) -> dict:
+    """Gradients of sum(dout * out) (see dash_attn_window_bwd): dq, dk, dv in the inputs' type.
+
+    out, lse: those of :func:`window_fwd`.  grads: optional dict of preallocated dq / dk / dv.
+    """
+    g = grads or {}
+    with _on(q, stream, k, v, out, lse, dout, seqlens, workspace, *g.values()) as s:
+        B, S, H, _ = q.shape
+        dq, dk, dv = (g[n] if n in g else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                      for n, t in (("dq", q), ("dk", k), ("dv", v)))
+        qd, kd, vd, od, dod, dqd, dkd, dvd = (ctypes.byref(_desc(t)) for t in (q, k, v, out, dout, dq, dk, dv))
+        ws = _scratch(_lib.dash_attn_window_bwd_workspace_size(qd, kd, window, sinks),
+                      "dash_attn_window_bwd_workspace_size", q.device, workspace)
+        _check(_lib.dash_attn_window_bwd(qd, kd, vd, od, _array(lse, "lse", (B, H, S), torch.float32), dod,
+                                         _array(seqlens, "seqlens", (B,)), window, sinks, dqd, dkd, dvd,
+                                         ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    return {"dq": dq, "dk": dk, "dv": dv}
+
+
+class _WindowAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks, seqlens):
+        out, lse = window_fwd(q, k, v, window, sinks, seqlens, return_lse=True)
+        ctx.save_for_backward(q, k, v, out, lse, seqlens)
+        ctx.args = (window, sinks)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse, seqlens = ctx.saved_tensors
+        g = window_bwd(q, k, v, out, lse, dout.contiguous(), *ctx.args, seqlens)
+        return g["dq"], g["dk"], g["dv"], None, None, None
+
+
+def window_attention(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None) -> torch.Tensor:
+    """Differentiable :func:`window_fwd`: forward by dash_attn_window_fwd, gradients by dash_attn_window_bwd."""
+    return _WindowAttention.apply(q, k, v, window, sinks, seqlens)
+
+
+def window_decode_workspace_size(heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace the one-token calls need on the current device (whatever the batch and the lengths)."""
+    return _lib.dash_attn_window_decode_workspace_size(heads, kv_heads, head_dim)
+
+
+def window_decode(q, kcache, vcache, seqlens, window: int = 0, sinks: int = 0, out=None, return_lse: bool = False,
+                  lse=None, workspace=None, stream=None):
+    """Attention of one new token per sequence, q [B, 1, H, d], over its cache (see dash_attn_window_decode)."""
+    return _window_decode(q, kcache, vcache, None, seqlens, window, sinks, out, return_lse, lse, workspace, stream)
+
+
+def window_decode_paged(q, k_pages, v_pages, block_table, seqlens, window: int = 0, sinks: int = 0, out=None,
+                        return_lse: bool = False, lse=None, workspace=None, stream=None):
+    """:func:`window_decode` against a paged cache (see dash_attn_window_decode_paged)."""
+    return _window_decode(q, k_pages, v_pages, block_table, seqlens, window, sinks, out, return_lse, lse, workspace,
+                          stream)
+
+
+def _window_decode(q, k, v, table, seqlens, window, sinks, out, return_lse, lse, workspace, stream):
+    with _on(q, stream, k, v, table, seqlens, out, lse, workspace) as s:
+        qd, kd, vd = _desc(q), _desc(k), _desc(v)
+        B, _, H, d = q.shape
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        if return_lse and lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        ws = _scratch(_lib.dash_attn_window_decode_workspace_size(H, kd.h, d),
+                      "dash_attn_window_decode_workspace_size", q.device, workspace)
+        head = (ctypes.byref(qd), ctypes.byref(kd), ctypes.byref(vd))
+        tail = (_array(seqlens, "seqlens", (B,)), window, sinks, ctypes.byref(_desc(out)),
+                _array(lse, "lse", (B, H), torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        if table is None:
+            _check(_lib.dash_attn_window_decode(*head, *tail))
+        else:
+            if table.dim() != 2:
+                raise ValueError("block_table must be [B, max_blocks]")
+            most = table.shape[1]
+            _check(_lib.dash_attn_window_decode_paged(*head, _array(table, "block_table", (B, most)), most, *tail))
+    return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------ cache pages
+
+
+def _pages_state(block_table, seqlens, refs):
+    """The arguments (table, batch, max_blocks, seqlens, refs, n_pages) of the calls on a block table."""
+    if block_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("block_table must be [batch, max_blocks] and refs [n_pages]")
+    batch, most = block_table.shape
+    return (_array(block_table, "block_table", (batch, most)), batch, most, _array(seqlens, "seqlens", (batch,)),
+            _array(refs, "refs", (refs.shape[0],)), refs.shape[0])
+
+
+def pages_workspace_size(batch: int, max_blocks: int, n_pages: int) -> int:
+    return _lib.dash_attn_pages_workspace_size(batch, max_blocks, n_pages)
+
+
+def _pages_scratch(state, device, given):
+    ws = _scratch(_lib.dash_attn_pages_workspace_size(state[1], state[2], state[5]), "dash_attn_pages_workspace_size",
+                  device, given)
+    return ws, (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def pages_fork(block_table, seqlens, refs, src, dst, block: int, workspace=None, stream=None) -> None:
+    """Sequences dst[i] become copies of src[i] that share their pages, in place (see dash_attn_pages_fork)."""
+    with _on(block_table, stream, seqlens, refs, src, dst, workspace) as s:
+        state = _pages_state(block_table, seqlens, refs)
+        n = dst.numel()
+        ws, room = _pages_scratch(state, block_table.device, workspace)
+        _check(_lib.dash_attn_pages_fork(*state, _array(src, "src", (n,)), _array(dst, "dst", (n,)), n, block, *room,
+                                         s))
+
+
+def pages_free(block_table, seqlens, refs, slots, block: int, workspace=None, stream=None) -> None:
+    """The sequences slots[i] give back their pages, in place (see dash_attn_pages_free)."""
+    with _on(block_table, stream, seqlens, refs, slots, workspace) as s:
+        state = _pages_state(block_table, seqlens, refs)
+        n = slots.numel()
+        ws, room = _pages_scratch(state, block_table.device, workspace)
+        _check(_lib.dash_attn_pages_free(*state, _array(slots, "slots", (n,)), n, block, *room, s))
+
+
+def pages_grow(block_table, seqlens, refs, n_new, block: int, workspace=None, stream=None):
+    """Room for n_new[b] more tokens of every sequence, in place (see dash_attn_pages_grow).
+
+    Returns copy_src, copy_dst [batch]: the page copies to make with :func:`pages_copy` before the new tokens are
+    written (-1: none).  When the pool has too few free pages nothing changes; pass a workspace to read that from
+    :func:`device_status`.
+    """
+    with _on(block_table, stream, seqlens, refs, n_new, workspace) as s:
+        state = _pages_state(block_table, seqlens, refs)
+        batch = state[1]
+        copies = torch.empty((2, batch), dtype=torch.int32, device=block_table.device)
+        ws, room = _pages_scratch(state, block_table.device, workspace)
+        _check(_lib.dash_attn_pages_grow(*state, _array(n_new, "n_new", (batch,)), block, copies[0].data_ptr(),
+                                         copies[1].data_ptr(), *room, s))
+    return copies[0], copies[1]
+
+
+def pages_compact(block_table, seqlens, refs, block: int, inplace: bool = False, workspace=None, stream=None) -> dict:
+    """The pages in use move to the low end of the pool (see dash_attn_pages_compact).
+
+    Returns table and refs after it (the inputs themselves with ``inplace``), the moves src, dst [n_pages // 2] to
+    make with :func:`pages_copy` (-1 past their number) and info [2] = {moves, pages in use}.
+    """
+    with _on(block_table, stream, seqlens, refs, workspace) as s:
+        state = _pages_state(block_table, seqlens, refs)
+        dev, n_pages = block_table.device, state[5]
+        table_out = block_table if inplace else torch.empty_like(block_table)
+        refs_out = refs if inplace else torch.empty_like(refs)
+        moves = torch.empty((2, n_pages // 2), dtype=torch.int32, device=dev)
+        info = torch.empty(2, dtype=torch.int32, device=dev)
+        ws, room = _pages_scratch(state, dev, workspace)
+        src, dst = moves[0], moves[1]
+        _check(_lib.dash_attn_pages_compact(*state, block, table_out.data_ptr(), refs_out.data_ptr(), src.data_ptr(),
+                                            dst.data_ptr(), info.data_ptr(), *room, s))
+    return {"table": table_out, "refs": refs_out, "src": src, "dst": dst, "info": info}
+
+
+def pages_copy(pools, src, dst, stream=None) -> None:
+    """Page src[i] of every pool [n_pages, s, h, d] to page dst[i] (see dash_attn_pages_copy)."""
+    pools = list(pools)
+    if not pools:
+        raise ValueError("no pools")
+    with _on(pools[0], stream, *pools[1:], src, dst) as s:
+        n = src.numel()
+        descs = (DashTensor * len(pools))(*[_desc(t) for t in pools])
+        _check(_lib.dash_attn_pages_copy(descs, len(pools), _array(src, "src", (n,)), _array(dst, "dst", (n,)), n, s))

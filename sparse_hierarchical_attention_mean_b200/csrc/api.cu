@@ -3,6 +3,7 @@
 // allocates no memory; work goes to the caller's stream.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -11,6 +12,7 @@
 #include "../../include/dashattn.h"
 #include "common.cuh"
 #include "internal.h"
+#include "window.h"
 
 namespace {
 
@@ -1311,6 +1313,420 @@ dash_status_t dash_attn_lists_to_mask(const int32_t* idx, const int32_t* cnt, in
   if (n_words > 128) return fail(DASH_ERR_UNSUPPORTED, "more than 4096 blocks per row");
   cudaError_t e = dash::launch_lists_to_mask(idx, cnt, rows, t_cap, mask, (int)n_words, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "lists to mask");
+  return ok();
+}
+
+// ------------------------------------------------------------------ dense / sliding-window attention
+
+namespace {
+
+// The view of a tensor for address arithmetic and TMA maps: the stride of an
+// extent of 1 is never multiplied, so it is given a valid value.
+dash::View solid_view(const dash_tensor_t* t) {
+  dash::View v = view(t);
+  if (t->h == 1) v.sh = t->d;
+  if (t->s == 1) v.ss = t->h * v.sh;
+  if (t->b == 1) v.sb = t->s * v.ss;
+  return v;
+}
+
+dash_status_t check_solid(const dash_tensor_t* t, const char* name) {
+  dash_status_t st;
+  if ((st = check_tensor(t, name))) return st;
+  if ((t->b > 1 && t->stride_b == 0) || (t->s > 1 && t->stride_s == 0) || (t->h > 1 && t->stride_h == 0))
+    return fail(DASH_ERR_UNSUPPORTED, "%s: a stride of 0 over an extent above 1", name);
+  return DASH_OK;
+}
+
+dash_status_t check_window(int64_t window, int64_t sinks) {
+  if (window < 0) return fail(DASH_ERR_INVALID_ARGUMENT, "window %lld < 0", (long long)window);
+  if (sinks < 0) return fail(DASH_ERR_INVALID_ARGUMENT, "sinks %lld < 0", (long long)sinks);
+  if (sinks > dash::kMaxSinks)
+    return fail(DASH_ERR_UNSUPPORTED, "sinks %lld above %d", (long long)sinks, dash::kMaxSinks);
+  return DASH_OK;
+}
+
+dash_status_t check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "workspace must be a 256-byte aligned device pointer");
+  if (bytes < need) return fail(DASH_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", bytes, need);
+  return DASH_OK;
+}
+
+dash_status_t check_like(const dash_tensor_t* t, const dash_tensor_t* like, const char* name) {
+  dash_status_t st;
+  if ((st = check_solid(t, name))) return st;
+  if (t->dtype != like->dtype) return fail(DASH_ERR_INVALID_ARGUMENT, "%s: dtype differs from q's", name);
+  if (t->b != like->b || t->s != like->s || t->h != like->h || t->d != like->d)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "%s: shape mismatch", name);
+  return DASH_OK;
+}
+
+dash_status_t check_window_qk(const dash_tensor_t* q, const dash_tensor_t* k) {
+  dash_status_t st;
+  if ((st = check_solid(q, "q")) || (st = check_solid(k, "k")) || (st = check_group(q->h, k->h))) return st;
+  if (q->dtype != k->dtype) return fail(DASH_ERR_INVALID_ARGUMENT, "q and k must share one dtype");
+  if (q->b != k->b || q->s != k->s || q->d != k->d) return fail(DASH_ERR_INVALID_ARGUMENT, "q and k shapes differ");
+  return DASH_OK;
+}
+
+struct WindowLayout {
+  size_t status, dd, total;
+};
+WindowLayout window_layout(const dash_tensor_t* q, const dash_tensor_t* k, int64_t window, int64_t sinks, bool bwd) {
+  WindowLayout L{};
+  (void)k;
+  (void)window;
+  (void)sinks;
+  L.status = 0;
+  L.dd = align256(sizeof(dash::DeviceStatus));
+  L.total = L.dd;
+  if (bwd) L.total = align256(L.dd + (size_t)q->b * q->h * q->s * 4);
+  return L;
+}
+
+dash::WindowParams window_params(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
+                                 const dash_tensor_t* out, const int32_t* seqlens, int64_t window, int64_t sinks,
+                                 float* lse) {
+  dash::WindowParams p{};
+  p.q = solid_view(q);
+  p.k = solid_view(k);
+  p.v = solid_view(v);
+  p.out = solid_view(out);
+  p.dtype = q->dtype;
+  p.B = (int)q->b;
+  p.S = (int)q->s;
+  p.H = (int)q->h;
+  p.Hkv = (int)k->h;
+  p.G = (int)(q->h / k->h);
+  p.D = (int)q->d;
+  const bool all = window == 0 || window >= q->s;
+  p.window = all ? p.S : (int)window;
+  p.sinks = all ? 0 : (int)std::min(sinks, q->s);
+  p.seqlens = seqlens;
+  p.lse = lse;
+  p.num_sms = num_sms();
+  return p;
+}
+
+}  // namespace
+
+size_t dash_attn_window_fwd_workspace_size(const dash_tensor_t* q, const dash_tensor_t* k) {
+  if (check_window_qk(q, k)) return 0;
+  return window_layout(q, k, 0, 0, false).total;
+}
+
+dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
+                                   const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+  dash_status_t st;
+  if ((st = check_window_qk(q, k)) || (st = check_like(v, k, "v")) || (st = check_like(out, q, "out")) ||
+      (st = check_window(window, sinks)))
+    return st;
+  const WindowLayout L = window_layout(q, k, window, sinks, false);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(dash::DeviceStatus), s);
+  if (e != cudaSuccess) return cuda_fail(e, "memset");
+  dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, lse);
+  p.status = at<dash::DeviceStatus>(workspace, L.status);
+  e = dash::launch_window_fwd_simt(p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "window forward");
+  return ok();
+}
+
+size_t dash_attn_window_bwd_workspace_size(const dash_tensor_t* q, const dash_tensor_t* k, int64_t window,
+                                           int64_t sinks) {
+  if (check_window_qk(q, k) || check_window(window, sinks)) return 0;
+  return window_layout(q, k, window, sinks, true).total;
+}
+
+dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
+                                   const dash_tensor_t* out, const float* lse, const dash_tensor_t* dout,
+                                   const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* dq,
+                                   dash_tensor_t* dk, dash_tensor_t* dv, void* workspace, size_t workspace_bytes,
+                                   dash_stream_t stream) {
+  dash_status_t st;
+  if ((st = check_window_qk(q, k)) || (st = check_like(v, k, "v")) || (st = check_like(out, q, "out")) ||
+      (st = check_like(dout, q, "dout")) || (st = check_like(dq, q, "dq")) || (st = check_like(dk, k, "dk")) ||
+      (st = check_like(dv, k, "dv")) || (st = check_window(window, sinks)))
+    return st;
+  if (!lse) return fail(DASH_ERR_INVALID_ARGUMENT, "null lse");
+  const WindowLayout L = window_layout(q, k, window, sinks, true);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(dash::DeviceStatus), s);
+  if (e != cudaSuccess) return cuda_fail(e, "memset");
+  dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, const_cast<float*>(lse));
+  p.dout = solid_view(dout);
+  p.dq = solid_view(dq);
+  p.dk = solid_view(dk);
+  p.dv = solid_view(dv);
+  p.dd = at<float>(workspace, L.dd);
+  p.status = at<dash::DeviceStatus>(workspace, L.status);
+  e = dash::launch_window_bwd_simt(p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "window backward");
+  return ok();
+}
+
+namespace {
+
+struct WindowDecodeLayout {
+  size_t status, cta_status, part_o, part_ml, total;
+  int n_cta;
+};
+WindowDecodeLayout window_decode_layout(int64_t G, int64_t D) {
+  WindowDecodeLayout L{};
+  L.n_cta = num_sms();
+  L.status = 0;
+  L.cta_status = align256(sizeof(dash::DeviceStatus));
+  L.part_o = align256(L.cta_status + (size_t)L.n_cta * 4);
+  L.part_ml = align256(L.part_o + (size_t)2 * L.n_cta * G * D * 4);
+  L.total = align256(L.part_ml + (size_t)2 * L.n_cta * G * 2 * 4);
+  return L;
+}
+
+dash_status_t run_window_decode(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
+                                const int32_t* table, int64_t max_blocks, int64_t lmax, const int32_t* seqlens,
+                                int64_t window, int64_t sinks, dash_tensor_t* out, float* lse, void* workspace,
+                                size_t workspace_bytes, dash_stream_t stream) {
+  dash_status_t st;
+  if ((st = check_solid(q, "q")) || (st = check_solid(k, table ? "k_pages" : "kcache")) ||
+      (st = check_like(v, k, table ? "v_pages" : "vcache")) || (st = check_like(out, q, "out")) ||
+      (st = check_group(q->h, k->h)) || (st = check_window(window, sinks)))
+    return st;
+  if (q->s != 1) return fail(DASH_ERR_INVALID_ARGUMENT, "decode takes one query token (s == 1)");
+  if (q->dtype == DASH_F32) return fail(DASH_ERR_UNSUPPORTED, "decode supports f16 and bf16");
+  if (q->dtype != k->dtype || q->d != k->d)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "the cache's dtype or head dim differs from q's");
+  if (!table && k->b != q->b) return fail(DASH_ERR_INVALID_ARGUMENT, "batch mismatch");
+  if (!seqlens) return fail(DASH_ERR_INVALID_ARGUMENT, "null seqlens");
+  if (lmax > (1ll << 30)) return fail(DASH_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+  const WindowDecodeLayout L = window_decode_layout(q->h / k->h, q->d);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
+  dash::WindowDecodeParams p{};
+  p.q = solid_view(q);
+  p.k = solid_view(k);
+  p.v = solid_view(v);
+  p.out = solid_view(out);
+  p.dtype = q->dtype;
+  p.B = (int)q->b;
+  p.H = (int)q->h;
+  p.Hkv = (int)k->h;
+  p.G = (int)(q->h / k->h);
+  p.D = (int)q->d;
+  p.Lmax = lmax;
+  p.window = window >= lmax ? 0 : (int)window;
+  p.sinks = p.window ? (int)sinks : 0;
+  p.seqlens = seqlens;
+  p.block_table = table;
+  p.max_blocks = (int)max_blocks;
+  p.block = (int)k->s;
+  p.n_pages = k->b;
+  p.lse = lse;
+  p.status = at<dash::DeviceStatus>(workspace, L.status);
+  p.cta_status = at<int32_t>(workspace, L.cta_status);
+  p.part_o = at<float>(workspace, L.part_o);
+  p.part_ml = at<float>(workspace, L.part_ml);
+  p.n_cta = L.n_cta;
+  cudaError_t e = dash::launch_window_decode(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "window decode");
+  return ok();
+}
+
+}  // namespace
+
+size_t dash_attn_window_decode_workspace_size(int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  if (heads <= 0 || check_group(heads, kv_heads) || (head_dim != 64 && head_dim != 128)) return 0;
+  return window_decode_layout(heads / kv_heads, head_dim).total;
+}
+
+dash_status_t dash_attn_window_decode(const dash_tensor_t* q, const dash_tensor_t* kcache, const dash_tensor_t* vcache,
+                                      const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* out,
+                                      float* lse, void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+  return run_window_decode(q, kcache, vcache, nullptr, 0, kcache ? kcache->s : 0, seqlens, window, sinks, out, lse,
+                           workspace, workspace_bytes, stream);
+}
+
+dash_status_t dash_attn_window_decode_paged(const dash_tensor_t* q, const dash_tensor_t* k_pages,
+                                            const dash_tensor_t* v_pages, const int32_t* block_table,
+                                            int64_t max_blocks, const int32_t* seqlens, int64_t window, int64_t sinks,
+                                            dash_tensor_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                            dash_stream_t stream) {
+  dash_status_t st;
+  if ((st = check_tensor(k_pages, "k_pages"))) return st;
+  if (k_pages->s != 64 && k_pages->s != 128)
+    return fail(DASH_ERR_UNSUPPORTED, "page size %lld not in {64, 128}", (long long)k_pages->s);
+  if (!block_table || max_blocks < 1)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "null block table or max_blocks < 1");
+  if (max_blocks > (1ll << 30) / k_pages->s) return fail(DASH_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+  return run_window_decode(q, k_pages, v_pages, block_table, max_blocks, max_blocks * k_pages->s, seqlens, window,
+                           sinks, out, lse, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ cache pages
+
+namespace {
+
+struct PagesLayout {
+  size_t status, list, aux, rows, total;
+};
+PagesLayout pages_layout(int64_t batch, int64_t max_blocks, int64_t n_pages) {
+  PagesLayout L{};
+  L.status = 0;
+  L.list = align256(sizeof(dash::DeviceStatus));
+  L.aux = align256(L.list + (size_t)n_pages * 4);
+  L.rows = align256(L.aux + (size_t)n_pages * 4);
+  L.total = align256(L.rows + (size_t)batch * max_blocks * 4);
+  return L;
+}
+
+dash_status_t check_page_sizes(int64_t batch, int64_t max_blocks, int64_t n_pages) {
+  if (batch < 1 || max_blocks < 1 || n_pages < 1)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "batch, max_blocks and n_pages must be positive");
+  if (batch > dash::kMaxPageSlots)
+    return fail(DASH_ERR_UNSUPPORTED, "more than %d sequences", dash::kMaxPageSlots);
+  if (max_blocks > (1ll << 30) / batch || n_pages > (1ll << 30))
+    return fail(DASH_ERR_UNSUPPORTED, "block table or pool above 2^30 entries");
+  return DASH_OK;
+}
+
+// The checks that the calls on a table share, and the parameters that they fill.
+dash_status_t begin_pages(const int32_t* table, int64_t batch, int64_t max_blocks, const int32_t* seqlens,
+                          const int32_t* refs, int64_t n_pages, int block, void* workspace, size_t workspace_bytes,
+                          dash::PagesParams* p) {
+  dash_status_t st;
+  if ((st = check_page_sizes(batch, max_blocks, n_pages))) return st;
+  if (block != 64 && block != 128) return fail(DASH_ERR_UNSUPPORTED, "block %d not in {64, 128}", block);
+  if (max_blocks > (1ll << 30) / block) return fail(DASH_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+  if (!table || !seqlens || !refs) return fail(DASH_ERR_INVALID_ARGUMENT, "null block table, seqlens or refs");
+  const PagesLayout L = pages_layout(batch, max_blocks, n_pages);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
+  *p = dash::PagesParams{};
+  p->table = const_cast<int32_t*>(table);
+  p->batch = batch;
+  p->max_blocks = max_blocks;
+  p->seqlens = const_cast<int32_t*>(seqlens);
+  p->refs = const_cast<int32_t*>(refs);
+  p->n_pages = n_pages;
+  p->block = block;
+  p->status = at<dash::DeviceStatus>(workspace, L.status);
+  p->list = at<int32_t>(workspace, L.list);
+  p->aux = at<int32_t>(workspace, L.aux);
+  p->rows = at<int32_t>(workspace, L.rows);
+  return DASH_OK;
+}
+
+}  // namespace
+
+size_t dash_attn_pages_workspace_size(int64_t batch, int64_t max_blocks, int64_t n_pages) {
+  if (check_page_sizes(batch, max_blocks, n_pages)) return 0;
+  return pages_layout(batch, max_blocks, n_pages).total;
+}
+
+static dash_status_t run_pages_fork(int32_t* block_table, int64_t batch, int64_t max_blocks, int32_t* seqlens,
+                                    int32_t* refs, int64_t n_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                                    int block, void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+  dash::PagesParams p;
+  dash_status_t st = begin_pages(block_table, batch, max_blocks, seqlens, refs, n_pages, block, workspace,
+                                 workspace_bytes, &p);
+  if (st) return st;
+  if (n < 0 || n > batch)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "%lld sequences of a table of %lld", (long long)n, (long long)batch);
+  p.src = src;
+  p.dst = dst;
+  p.n = (int)n;
+  cudaError_t e = dash::launch_pages_fork(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages fork");
+  return ok();
+}
+
+dash_status_t dash_attn_pages_fork(int32_t* block_table, int64_t batch, int64_t max_blocks, int32_t* seqlens,
+                                   int32_t* refs, int64_t n_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                                   int block, void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+  if (n > 0 && (!src || !dst)) return fail(DASH_ERR_INVALID_ARGUMENT, "null src or dst");
+  return run_pages_fork(block_table, batch, max_blocks, seqlens, refs, n_pages, src, dst, n, block, workspace,
+                        workspace_bytes, stream);
+}
+
+dash_status_t dash_attn_pages_free(int32_t* block_table, int64_t batch, int64_t max_blocks, int32_t* seqlens,
+                                   int32_t* refs, int64_t n_pages, const int32_t* slots, int64_t n, int block,
+                                   void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+  if (n > 0 && !slots) return fail(DASH_ERR_INVALID_ARGUMENT, "null slots");
+  return run_pages_fork(block_table, batch, max_blocks, seqlens, refs, n_pages, nullptr, slots, n, block, workspace,
+                        workspace_bytes, stream);
+}
+
+dash_status_t dash_attn_pages_grow(int32_t* block_table, int64_t batch, int64_t max_blocks, int32_t* seqlens,
+                                   int32_t* refs, int64_t n_pages, const int32_t* n_new, int block, int32_t* copy_src,
+                                   int32_t* copy_dst, void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+  dash::PagesParams p;
+  dash_status_t st = begin_pages(block_table, batch, max_blocks, seqlens, refs, n_pages, block, workspace,
+                                 workspace_bytes, &p);
+  if (st) return st;
+  if (!n_new || !copy_src || !copy_dst)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "null n_new, copy_src or copy_dst");
+  p.n_new = n_new;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  cudaError_t e = dash::launch_pages_grow(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages grow");
+  return ok();
+}
+
+dash_status_t dash_attn_pages_compact(const int32_t* block_table, int64_t batch, int64_t max_blocks,
+                                      const int32_t* seqlens, const int32_t* refs, int64_t n_pages, int block,
+                                      int32_t* table_out, int32_t* refs_out, int32_t* move_src, int32_t* move_dst,
+                                      int32_t* info, void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+  dash::PagesParams p;
+  dash_status_t st = begin_pages(block_table, batch, max_blocks, seqlens, refs, n_pages, block, workspace,
+                                 workspace_bytes, &p);
+  if (st) return st;
+  if (!table_out || !refs_out || !info || (n_pages > 1 && (!move_src || !move_dst)))
+    return fail(DASH_ERR_INVALID_ARGUMENT, "null table_out, refs_out, move_src, move_dst or info");
+  p.table_out = table_out;
+  p.refs_out = refs_out;
+  p.move_src = move_src;
+  p.move_dst = move_dst;
+  p.info = info;
+  cudaError_t e = dash::launch_pages_compact(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages compact");
+  return ok();
+}
+
+dash_status_t dash_attn_pages_copy(const dash_tensor_t* pools, int64_t n_pools, const int32_t* src,
+                                   const int32_t* dst, int64_t n, dash_stream_t stream) {
+  if (n_pools < 1 || n_pools > dash::kMaxPools || !pools)
+    return fail(DASH_ERR_INVALID_ARGUMENT, "pools: 1 to %d of them", dash::kMaxPools);
+  if (n < 0 || (n > 0 && (!src || !dst))) return fail(DASH_ERR_INVALID_ARGUMENT, "n < 0, or null src or dst");
+  dash::PageCopyParams p{};
+  const dash_tensor_t& first = pools[0];
+  bool flat = true;
+  for (int64_t i = 0; i < n_pools; ++i) {
+    const dash_tensor_t& t = pools[i];
+    dash_status_t st;
+    if ((st = check_solid(&t, "pool"))) return st;
+    if (t.dtype != first.dtype || t.s != first.s || t.h != first.h || t.d != first.d)
+      return fail(DASH_ERR_INVALID_ARGUMENT, "pools of different dtypes or page shapes");
+    const dash::View v = solid_view(&t);
+    const int64_t es = elt_size(t.dtype);
+    p.pool[i] = dash::PagePool{static_cast<char*>(t.data), t.b, v.sb * es, v.ss * es, v.sh * es};
+    // either order of tokens and heads fills the page without gaps
+    flat = flat && ((v.sh == t.d && v.ss == t.h * t.d) || (v.ss == t.d && v.sh == t.s * t.d));
+  }
+  const int64_t bytes = first.s * first.h * first.d * elt_size(first.dtype);
+  if (bytes > (1ll << 30)) return fail(DASH_ERR_UNSUPPORTED, "pages above 1 GiB");
+  if (n == 0) return ok();
+  p.n_pools = (int)n_pools;
+  p.rows = flat ? 1 : (int)first.s;
+  p.heads = flat ? 1 : (int)first.h;
+  p.run = flat ? bytes : first.d * elt_size(first.dtype);
+  p.src = src;
+  p.dst = dst;
+  p.n = n;
+  if (!dash::pages_copy_fits(p)) return fail(DASH_ERR_UNSUPPORTED, "too many pages in one call");
+  cudaError_t e = dash::launch_pages_copy(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages copy");
   return ok();
 }
 

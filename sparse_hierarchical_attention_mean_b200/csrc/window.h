@@ -1,0 +1,132 @@
+// Parameters of the sliding-window attention kernels (forward, backward and
+// one-token decode) and of the cache page kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace dash {
+
+// Causal attention of row i over the keys j <= i with j > i - window or
+// j < sinks.  The host passes window in [1, S] (S: every key) and sinks in
+// [0, kMaxSinks], 0 when the window hides nothing.
+constexpr int kMaxSinks = 128;
+
+struct WindowParams {
+  View q, k, v, out;        // [B, S, H or Hkv, D], dtype
+  View dout, dq, dk, dv;    // backward, dtype
+  int dtype;
+  int B, S, H, Hkv, G, D;
+  int window, sinks;
+  const int32_t* seqlens;   // [B] or null: rows and keys from seqlens[b] on are not there
+  float* lse;               // [B, H, S] natural log-sum-exp of the row's logits, or null
+  float* dd;                // [B, H, S] dout . out (backward)
+  float* part;              // sink partials (backward, tensor-core path)
+  int n_chunks;             // query chunks of the sink keys (backward, tensor-core path)
+  int num_sms;
+  DeviceStatus* status;
+};
+
+// Tiles of `step` keys that rows [r0, r1) see: first the sink tiles that end
+// before the band, then the band.
+struct KeyTiles {
+  int n_sink, band0, n;
+  __host__ __device__ KeyTiles(int r0, int r1, int window, int sinks, int step) {
+    const int lo = r0 - window + 1;
+    band0 = (lo > 0 ? lo : 0) / step;
+    const int s = (sinks + step - 1) / step;
+    n_sink = s < band0 ? s : band0;
+    n = n_sink + (r1 + step - 1) / step - band0;
+  }
+  __host__ __device__ int tile(int i) const { return i < n_sink ? i : band0 + i - n_sink; }
+};
+
+// Valid length of sequence b (clamped to [0, S]; reported when out of range).
+__device__ __forceinline__ int window_len(const WindowParams& p, int b) {
+  if (!p.seqlens) return p.S;
+  const int n = p.seqlens[b];
+  if (n < 0 || n > p.S) raise_status(p.status, 1 /* DASH_ERR_INVALID_ARGUMENT */, 301);
+  return min(max(n, 0), p.S);
+}
+
+// fp32 CUDA-core path
+cudaError_t launch_window_fwd_simt(const WindowParams& p, cudaStream_t stream);
+cudaError_t launch_window_bwd_simt(const WindowParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- decode
+struct WindowDecodeParams {
+  View q, k, v, out;           // q, out [B, 1, H, D]; k, v [B, Lmax, Hkv, D] or pages [n_pages, block, Hkv, D]
+  int dtype;
+  int B, H, Hkv, G, D;
+  int64_t Lmax;                // tokens a sequence may hold
+  int window, sinks;           // window 0: every token
+  const int32_t* seqlens;      // [B]
+  const int32_t* block_table;  // [B, max_blocks], or null: dense cache
+  int max_blocks, block;       // block: tokens per page
+  int64_t n_pages;             // extent of the outermost dimension of k / v
+  float* lse;                  // [B, H] natural log-sum-exp, or null
+  // workspace
+  DeviceStatus* status;
+  int32_t* cta_status;         // [n_cta] what each streaming CTA saw (0: nothing wrong)
+  float* part_o;               // [2 n_cta, G, D] unnormalised partial outputs
+  float* part_ml;              // [2 n_cta, G, 2] their reference max (log2 units) and sum
+  int n_cta;
+};
+cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- cache pages
+// refs[p]: how many table entries hold page p (0: free).  Sequence b holds
+// the first ceil(seqlens[b] / block) entries of its row.
+constexpr int kMaxPageSlots = 8192;  // sequences of one table
+struct PagesParams {
+  int32_t* table;  // [batch, max_blocks]
+  int64_t batch, max_blocks;
+  int32_t* seqlens;  // [batch]
+  int32_t* refs;     // [n_pages]
+  int64_t n_pages;
+  int block;
+  // fork / free: row dst[i] becomes a copy of row src[i] (src null: empty)
+  const int32_t* src;
+  const int32_t* dst;
+  int n;
+  // grow: tokens to make room for, and the copies of shared last pages
+  const int32_t* n_new;  // [batch]
+  int32_t* copy_src;     // [batch]
+  int32_t* copy_dst;     // [batch]
+  // compact
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* move_src;  // [n_pages / 2]
+  int32_t* move_dst;  // [n_pages / 2]
+  int32_t* info;      // {moves, pages held}
+  // workspace
+  int32_t* list;  // [n_pages] (grow: the pages handed out; compact: where each page went)
+  int32_t* aux;   // [n_pages] (compact: refs of the moved pages)
+  int32_t* rows;  // [batch, max_blocks] (fork: the source rows, when one is overwritten)
+  DeviceStatus* status;
+};
+cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_grow(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t stream);
+
+// One pool: pages of `rows` x `heads` runs of `run` bytes (rows = heads = 1:
+// a page is one run).
+constexpr int kMaxPools = 64;
+struct PagePool {
+  char* data;
+  int64_t n_pages, page_stride, row_stride, head_stride;  // bytes
+};
+struct PageCopyParams {
+  PagePool pool[kMaxPools];
+  int n_pools, rows, heads;
+  int64_t run;  // bytes, a multiple of 16
+  const int32_t* src;
+  const int32_t* dst;
+  int64_t n;
+};
+bool pages_copy_fits(const PageCopyParams& p);  // one launch's grid holds the call
+cudaError_t launch_pages_copy(const PageCopyParams& p, cudaStream_t stream);
+
+}  // namespace dash

@@ -1,0 +1,504 @@
+// Attention of one new token per sequence over its KV cache (dense or paged),
+// whole context or sliding window + first tokens, split over the cache.
+//
+// The token of sequence b stands at L - 1 (L = seqlens[b]) and sees the
+// tokens t < L with t >= L - window or t < sinks:
+//   o_h = sum_t p_t v_t / sum_t p_t,  p_t = 2^(q_h . k_t log2(e) / sqrt(D) - m)
+//
+// Bound by reading the visible K and V once.  The unit of work is a step of
+// 64 tokens of one (sequence, KV head); the steps of all of them, in order,
+// are one line that is cut into equal parts, one per CTA, so every SM streams
+// the same number of bytes whatever the lengths.  A CTA is one producer warp,
+// which fills a ring of shared-memory stages (K and V of a step, two TMA
+// copies each at D = 128; the block table is read 32 entries at a time), and four
+// consumer warps that own 16 tokens of each step.  A (sequence, KV head) that
+// falls into one CTA is finished there; one that a cut divides leaves a
+// partial (o, m, l) per CTA, at most two per CTA, and the join kernel merges
+// them in order (the result does not depend on timing).
+//
+// G <= 8 query heads are the rows of a warp-level m16n8k16 MMA (half of it is
+// padding: the products need 1% of the tensor rate, the 64-row minimum of
+// tcgen05 would waste eight times that).  P is rounded to the cache's type
+// for the second product (as FlashAttention-like kernels do: relative error
+// half a step of that type per term, averaged over the sum); m, l and o are
+// fp32.
+//
+// What stands in the cache at masked tokens is never used: masked logits are
+// replaced before the maximum, and masked V values are cleared in registers
+// (only in the steps that hold a mask's edge), so NaN there is harmless.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "mma_sync.cuh"
+#include "tc.cuh"
+#include "window.h"
+
+namespace dash {
+namespace {
+
+constexpr int kStep = 64;
+constexpr int kConsumers = 4;
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kMinUnits = 2;  // steps a CTA takes at least, before more CTAs share the work
+
+template <int D>
+struct Layout {
+  static constexpr int KC = D / 64;
+  static constexpr int kChunk = kStep * 128;         // 64 tokens x 128 bytes
+  static constexpr int kTile = KC * kChunk;          // K (or V) of a step
+  static constexpr int kStages = D == 128 ? 6 : 12;  // 192 KB in flight per SM
+  static constexpr int kOffO = 2 * kStages * kTile;  // merge buffer [4][8][D] fp32
+  static constexpr int kOffMl = kOffO + kConsumers * 8 * D * 4;
+  static constexpr int kOffBar = kOffMl + kConsumers * 8 * 2 * 4;
+  static constexpr int kBytes = kOffBar + 2 * kStages * 8 + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+// The steps of one sequence: sink tiles that end before the band, then the band.
+struct SeqSteps {
+  int L, lo, n_sink, band0, n;
+  __device__ SeqSteps(const WindowDecodeParams& p, int b) {
+    const int raw = p.seqlens[b];
+    L = (int)min((int64_t)max(raw, 0), p.Lmax);
+    lo = p.window > 0 ? max(0, L - p.window) : 0;
+    band0 = lo / kStep;
+    n_sink = min((p.sinks + kStep - 1) / kStep, band0);
+    n = n_sink + (L + kStep - 1) / kStep - band0;
+  }
+  __device__ int tok0(int s) const { return (s < n_sink ? s : band0 + s - n_sink) * kStep; }
+};
+
+// Steps of the sequences [b0, b0 + 32), one per lane (0 past the batch).
+__device__ __forceinline__ int lane_steps(const WindowDecodeParams& p, int b0, int lane) {
+  return b0 + lane < p.B ? SeqSteps(p, b0 + lane).n : 0;
+}
+
+__device__ __forceinline__ long long warp_sum_ll(long long x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Steps of the whole batch per KV head (every lane of a warp calls it), and
+// the steps of the sequences before b.
+__device__ __forceinline__ void batch_steps(const WindowDecodeParams& p, int b, int lane, long long* total,
+                                            long long* before) {
+  long long t = 0, f = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int n = lane_steps(p, b0, lane);
+    t += n;
+    if (b0 + lane < b) f += n;
+  }
+  *total = warp_sum_ll(t);
+  if (before) *before = warp_sum_ll(f);
+}
+
+// How the line of `units` steps is cut: part c is [c units / n, (c + 1) units / n).
+struct Cut {
+  long long units;
+  int n;
+  __device__ Cut(long long u, int n_cta) : units(u) {
+    const long long want = (u + kMinUnits - 1) / kMinUnits;
+    n = (int)max(1ll, min((long long)n_cta, want));
+  }
+  __device__ long long start(int c) const { return units * c / n; }
+  __device__ int owner(long long u) const { return (int)(((u + 1) * n - 1) / units); }
+};
+
+// Walks a part of the line: the (sequence, KV head) segments in order.
+struct Walk {
+  int b, g, s0, s1;    // segment: steps [s0, s1) of (b, g)
+  bool whole;          // the segment is all of (b, g)
+  bool head;           // it starts before this part
+  long long left;      // steps of the part from s0 on
+  __device__ bool begin(const WindowDecodeParams& p, const Cut& cut, int c, int lane) {
+    long long u = cut.start(c);
+    left = cut.start(c + 1) - u;
+    if (c >= cut.n || left <= 0) return false;
+    // the sequence that holds step u
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const long long n = (long long)lane_steps(p, b0, lane) * p.Hkv;
+      long long inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u);
+      if (hit) {
+        const int w = __ffs(hit) - 1;
+        const long long first = base + __shfl_sync(0xffffffffu, inc - n, w);
+        const int steps = (int)(__shfl_sync(0xffffffffu, n, w) / p.Hkv);
+        b = b0 + w;
+        g = (int)((u - first) / steps);
+        s0 = (int)((u - first) % steps);
+        return true;
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return false;
+  }
+  __device__ void open(const SeqSteps& q) {
+    s1 = (int)min((long long)q.n, s0 + left);
+    whole = s0 == 0 && s1 == q.n;
+    head = s0 > 0;
+  }
+  // to the next segment; false at the end of the part
+  __device__ bool next(const WindowDecodeParams& p, SeqSteps& q) {
+    left -= s1 - s0;
+    if (left <= 0) return false;
+    s0 = 0;
+    if (++g == p.Hkv) {
+      g = 0;
+      do {
+        ++b;
+        q = SeqSteps(p, b);
+      } while (q.n == 0);
+    }
+    return true;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const WindowDecodeParams p) {
+  using L = Layout<D>;
+  constexpr int kStages = L::kStages;
+  constexpr int KS = D / 16;  // k slices of S = Q K^T
+  constexpr int NT = D / 8;   // 8-wide tiles of O
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* obuf = reinterpret_cast<float*>(smem + L::kOffO);
+  float* mlbuf = reinterpret_cast<float*>(smem + L::kOffMl);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* empty = full + kStages;
+  int* bad = reinterpret_cast<int*>(empty + kStages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], kConsumers);
+    }
+    *bad = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == kConsumers && lane == 0) {
+    tc::prefetch_tensormap(&tm_k);
+    tc::prefetch_tensormap(&tm_v);
+  }
+  __syncthreads();
+
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  long long total;
+  batch_steps(p, 0, lane, &total, nullptr);
+  const Cut cut(total * p.Hkv, p.n_cta);
+  Walk w;
+  const bool any = total > 0 && w.begin(p, cut, blockIdx.x, lane);
+
+  if (any && warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    SeqSteps q(p, w.b);
+    int i = 0, pages = 0;
+    bool ok = true;
+    do {
+      w.open(q);
+      for (int s = w.s0; ok && s < w.s1; ++s) {
+        const int tok = q.tok0(s);
+        int c2 = tok, c3 = w.b;
+        if (p.block_table) {
+          // 32 page numbers at a time, one per lane
+          if (((s - w.s0) & 31) == 0)
+            pages = s + lane < w.s1
+                        ? __ldg(p.block_table + (int64_t)w.b * p.max_blocks + q.tok0(s + lane) / p.block)
+                        : 0;
+          const int page = __shfl_sync(0xffffffffu, pages, (s - w.s0) & 31);
+          c2 = tok % p.block;
+          c3 = page;
+          if (page < 0 || page >= p.n_pages) {
+            if (lane == 0) atomicMax(bad, 1 /* DASH_ERR_INVALID_ARGUMENT */);
+            c3 = (int)p.n_pages;  // past the pool's end: the copy fills the stage with zeros
+          }
+        }
+        const int st = i % kStages;
+        if (i >= kStages) ok = tc::mbar_wait(&empty[st], ((i / kStages) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(&full[st], 2 * L::kTile);
+#pragma unroll
+          for (int kc = 0; kc < L::KC; ++kc) {
+            uint8_t* dst = smem + st * 2 * L::kTile + kc * L::kChunk;
+            tc::tma_load_4d(dst, &tm_k, &full[st], kc * 64, w.g, c2, c3);
+            tc::tma_load_4d(dst + L::kTile, &tm_v, &full[st], kc * 64, w.g, c2, c3);
+          }
+        }
+        ++i;
+      }
+    } while (ok && w.next(p, q));
+    if (!ok && lane == 0) atomicMax(bad, 5 /* DASH_ERR_DEVICE_TIMEOUT */);
+    // every copy lands before the CTA retires
+    for (int j = i > kStages ? i - kStages : 0; j < i; ++j) tc::mbar_wait(&full[j % kStages], (j / kStages) & 1);
+  } else if (any) {
+    // ------------------------------------------------------------ consumers
+    const int G = p.G, gq = lane >> 2, tq = lane & 3;
+    const float qk_scale = rsqrtf((float)D) * kLog2e;
+    SeqSteps q(p, w.b);
+    int i = 0;
+    bool ok = true;
+    do {
+      w.open(q);
+      // A fragments of the query heads (rows gq >= G and 8..15 are zero)
+      uint32_t qa[KS][2];
+      {
+        const T* src = static_cast<const T*>(p.q.data) + (int64_t)w.b * p.q.sb + (int64_t)(w.g * G + gq) * p.q.sh;
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+          qa[kk][0] = gq < G ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * tq) : 0u;
+          qa[kk][1] = gq < G ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * tq) : 0u;
+        }
+      }
+      float o[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      float m_used = kNegInf, lpart = 0.f;
+      for (int s = w.s0; s < w.s1; ++s, ++i) {
+        const int st = i % kStages;
+        // a wait that ran out ends this warp's work, but not its part in the
+        // CTA's named barriers below
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&full[st], (i / kStages) & 1));
+        if (!ok) break;
+        const uint32_t kst = smem_u32(smem + st * 2 * L::kTile), vst = kst + L::kTile;
+        // S = Q K^T of this warp's 16 tokens
+        float sacc[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) sacc[n][0] = sacc[n][1] = sacc[n][2] = sacc[n][3] = 0.f;
+        {
+          const int mt = lane >> 3, rr = lane & 7;
+          const int row = warp * 16 + (mt >> 1) * 8 + rr;
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+            const int c = 2 * (kk & 3) + (mt & 1);
+            uint32_t bf[4];
+            ldsm_x4(kst + (kk >> 2) * L::kChunk + row * 128 + ((c ^ (row & 7)) << 4), bf);
+            const uint32_t a[4] = {qa[kk][0], 0u, qa[kk][1], 0u};
+            mma16816<T>(sacc[0], a, bf[0], bf[1]);
+            mma16816<T>(sacc[1], a, bf[2], bf[3]);
+          }
+        }
+        // logits of head gq (log2 units) for tokens 2tq, 2tq + 1, 8 + 2tq, 9 + 2tq
+        const int tok0 = q.tok0(s);
+        const bool edge = tok0 + kStep > q.L || tok0 < q.lo;  // some token of the step may be hidden
+        float x[4];
+        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = sacc[e >> 1][e & 1] * qk_scale;
+        if (edge) {
+          bool seen[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = tok0 + warp * 16 + (e >> 1) * 8 + 2 * tq + (e & 1);
+            seen[e] = t < q.L && (t >= q.lo || t < p.sinks);
+            if (!seen[e]) x[e] = kNegInf;
+          }
+          vm0 = (seen[0] ? 0xffffu : 0u) | (seen[1] ? 0xffff0000u : 0u);
+          vm1 = (seen[2] ? 0xffffu : 0u) | (seen[3] ? 0xffff0000u : 0u);
+        }
+        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float corr = 1.0f;
+        bool resc = false;
+        if (mx != kNegInf) {
+          if (m_used == kNegInf) {
+            m_used = mx;
+          } else if (mx > m_used + 8.0f) {  // P stays <= 2^8, in range of both types
+            corr = tc::ex2(m_used - mx);
+            m_used = mx;
+            resc = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[n][0] *= corr;
+            o[n][1] *= corr;
+          }
+          lpart *= corr;
+        }
+        float pe[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pe[e] = m_used == kNegInf ? 0.f : tc::ex2(x[e] - m_used);
+        lpart += (pe[0] + pe[1]) + (pe[2] + pe[3]);
+        const uint32_t pa[4] = {pack2<T>(pe[0], pe[1]), 0u, pack2<T>(pe[2], pe[3]), 0u};
+        // O += P V
+        {
+          const int mt = lane >> 3, rr = lane & 7;
+          const int row = warp * 16 + (mt & 1) * 8 + rr;
+#pragma unroll
+          for (int j = 0; j < NT / 2; ++j) {
+            const int c = 2 * j + (mt >> 1);
+            uint32_t bf[4];
+            ldsm_x4_t(vst + (c >> 3) * L::kChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4), bf);
+            if (edge) {
+              bf[0] &= vm0;
+              bf[1] &= vm1;
+              bf[2] &= vm0;
+              bf[3] &= vm1;
+            }
+            mma16816<T>(o[2 * j], pa, bf[0], bf[1]);
+            mma16816<T>(o[2 * j + 1], pa, bf[2], bf[3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&empty[st]);
+      }
+      // merge the four warps
+      float l = lpart;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (gq < G) {
+        if (tq == 0) {
+          mlbuf[(warp * 8 + gq) * 2] = m_used;
+          mlbuf[(warp * 8 + gq) * 2 + 1] = l;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<float2*>(obuf + (warp * 8 + gq) * D + n * 8 + 2 * tq) = make_float2(o[n][0], o[n][1]);
+      }
+      asm volatile("bar.sync 1, %0;\n" ::"n"(kConsumers * 32) : "memory");
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (w.head ? 0 : 1);
+      for (int e = threadIdx.x * 2; e < G * D; e += kConsumers * 64) {
+        const int h = e / D, c = e % D;
+        float M = kNegInf;
+#pragma unroll
+        for (int u = 0; u < kConsumers; ++u) M = fmaxf(M, mlbuf[(u * 8 + h) * 2]);
+        const float Mu = M == kNegInf ? 0.f : M;
+        float a0 = 0.f, a1 = 0.f, sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < kConsumers; ++u) {
+          const float f = tc::ex2(mlbuf[(u * 8 + h) * 2] - Mu);
+          const float2 ov = *reinterpret_cast<const float2*>(obuf + (u * 8 + h) * D + c);
+          a0 = fmaf(f, ov.x, a0);
+          a1 = fmaf(f, ov.y, a1);
+          sum = fmaf(f, mlbuf[(u * 8 + h) * 2 + 1], sum);
+        }
+        if (w.whole) {
+          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays NaN
+          const int head = w.g * G + h;
+          T* dst = static_cast<T*>(const_cast<void*>(p.out.data)) + (int64_t)w.b * p.out.sb + (int64_t)head * p.out.sh;
+          *reinterpret_cast<uint32_t*>(dst + c) = pack2<T>(a0 * inv, a1 * inv);
+          if (p.lse && c == 0)
+            p.lse[(int64_t)w.b * p.H + head] = sum == 0.f ? kNegInf : (M + log2f(sum)) / kLog2e;
+        } else {
+          *reinterpret_cast<float2*>(p.part_o + (slot * G + h) * D + c) = make_float2(a0, a1);
+          if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * G + h) * 2) = make_float2(M, sum);
+        }
+      }
+      asm volatile("bar.sync 1, %0;\n" ::"n"(kConsumers * 32) : "memory");
+    } while (w.next(p, q));
+    if (!ok && lane == 0) atomicMax(bad, 5 /* DASH_ERR_DEVICE_TIMEOUT */);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) p.cta_status[blockIdx.x] = *bad;
+}
+
+// One CTA per (KV head, sequence): merges the partials of a divided one in
+// order, writes zeros for a sequence without tokens; the first CTA also
+// writes the status word.
+template <typename T>
+__global__ void __launch_bounds__(128) window_decode_join_kernel(const WindowDecodeParams p) {
+  const int g = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31;
+  const int G = p.G, D = p.D;
+  long long total, before;
+  batch_steps(p, b, lane, &total, &before);
+  const SeqSteps q(p, b);
+  const Cut cut(total * p.Hkv, p.n_cta);
+  const long long u0 = before * p.Hkv + (long long)g * q.n;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (g == 0 && b == 0 && threadIdx.x < 32) {
+    int code = 0;
+    for (int c = lane; c < p.n_cta; c += 32) code = max(code, p.cta_status[c]);
+    for (int i = lane; i < p.B; i += 32)
+      if (p.seqlens[i] < 0 || p.seqlens[i] > p.Lmax) code = max(code, 1 /* DASH_ERR_INVALID_ARGUMENT */);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) code = max(code, __shfl_xor_sync(0xffffffffu, code, o));
+    if (lane == 0) {
+      p.status->code = code;
+      p.status->detail = code ? 311 : 0;
+    }
+  }
+  T* dst = static_cast<T*>(const_cast<void*>(p.out.data)) + (int64_t)b * p.out.sb + (int64_t)g * G * p.out.sh;
+  if (q.n == 0) {
+    for (int e = threadIdx.x * 2; e < G * D; e += 256) {
+      *reinterpret_cast<uint32_t*>(dst + (int64_t)(e / D) * p.out.sh + e % D) = 0u;
+      if (p.lse && e % D == 0) p.lse[(int64_t)b * p.H + g * G + e / D] = kNegInf;
+    }
+    return;
+  }
+  const int c0 = cut.owner(u0), c1 = cut.owner(u0 + q.n - 1);
+  if (c0 == c1) return;  // finished by its CTA
+  for (int e = threadIdx.x * 2; e < G * D; e += 256) {
+    const int h = e / D, c = e % D;
+    float M = kNegInf;
+    for (int u = c0; u <= c1; ++u) {
+      const int64_t slot = 2 * (int64_t)u + (u == c0 ? 1 : 0);
+      M = fmaxf(M, p.part_ml[(slot * G + h) * 2]);
+    }
+    const float Mu = M == kNegInf ? 0.f : M;
+    float a0 = 0.f, a1 = 0.f, sum = 0.f;
+    for (int u = c0; u <= c1; ++u) {
+      const int64_t slot = 2 * (int64_t)u + (u == c0 ? 1 : 0);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * G + h) * 2);
+      const float2 ov = *reinterpret_cast<const float2*>(p.part_o + (slot * G + h) * D + c);
+      const float f = tc::ex2(ml.x - Mu);
+      a0 = fmaf(f, ov.x, a0);
+      a1 = fmaf(f, ov.y, a1);
+      sum = fmaf(f, ml.y, sum);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    *reinterpret_cast<uint32_t*>(dst + (int64_t)h * p.out.sh + c) = pack2<T>(a0 * inv, a1 * inv);
+    if (p.lse && c == 0)
+      p.lse[(int64_t)b * p.H + g * G + h] = sum == 0.f ? kNegInf : (M + log2f(sum)) / kLog2e;
+  }
+}
+
+template <typename T, int D>
+cudaError_t run(const WindowDecodeParams& p, cudaStream_t stream) {
+  using L = Layout<D>;
+  CUtensorMap mk, mv;
+  const int64_t rows = p.block_table ? p.block : p.Lmax, outer = p.block_table ? p.n_pages : p.B;
+  if (!make_map(&mk, p.k, p.dtype, outer, rows, p.Hkv, D, 1, kStep) ||
+      !make_map(&mv, p.v, p.dtype, outer, rows, p.Hkv, D, 1, kStep))
+    return cudaErrorInvalidValue;
+  auto kern = window_decode_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  kern<<<p.n_cta, kThreads, L::kAlloc, stream>>>(mk, mv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // the join's launch overlaps the streaming kernel's end; it waits for its results itself
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.Hkv, p.B);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, window_decode_join_kernel<T>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream) {
+  if (p.D == 128)
+    return p.dtype == 1 ? run<__half, 128>(p, stream) : run<__nv_bfloat16, 128>(p, stream);
+  return p.dtype == 1 ? run<__half, 64>(p, stream) : run<__nv_bfloat16, 64>(p, stream);
+}
+
+}  // namespace dash
