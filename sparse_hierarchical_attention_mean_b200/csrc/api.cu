@@ -1430,7 +1430,7 @@ dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* 
   if (e != cudaSuccess) return cuda_fail(e, "memset");
   dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, lse);
   p.status = at<dash::DeviceStatus>(workspace, L.status);
-  e = dash::launch_window_fwd_simt(p, s);
+  e = q->dtype == DASH_F32 ? dash::launch_window_fwd_simt(p, s) : dash::launch_window_fwd_tc(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "window forward");
   return ok();
 }

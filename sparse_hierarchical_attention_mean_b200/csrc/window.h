@@ -51,6 +51,8 @@ __device__ __forceinline__ int window_len(const WindowParams& p, int b) {
   return min(max(n, 0), p.S);
 }
 
+// f16 / bf16 tensor-core path
+cudaError_t launch_window_fwd_tc(const WindowParams& p, cudaStream_t stream);
 // fp32 CUDA-core path
 cudaError_t launch_window_fwd_simt(const WindowParams& p, cudaStream_t stream);
 cudaError_t launch_window_bwd_simt(const WindowParams& p, cudaStream_t stream);

@@ -1,0 +1,420 @@
+// Sliding-window (and dense causal) attention forward on the 5th-generation
+// tensor cores, f16 / bf16.
+//
+// Row i of head h sees key j when j <= i and (j > i - window or j < sinks):
+//   s_ij = q_i . k_j / sqrt(D);  o_i = sum_j 2^(s_ij log2e - m) v_j / l
+//
+// A tile is 128 rows = (128 / G positions) x (G heads of one KV group), so
+// each K/V tile serves the group's heads and a tile's band is narrow: its keys
+// are the window plus 128 / G.  A work item is two adjacent tiles of one KV
+// head; each CTA (one per SM) walks items.  Per item the keys come in steps of
+// 128: at most one step of sink tokens before the band, then the band; only
+// steps that hold a visible pair are walked, and only steps at an edge of the
+// band are masked (bit masks per row).
+//
+// Tensor memory: S of tile t at 128 t (P written back over it in 16 bits), O
+// of tile t at 256 + 128 t.  Shared memory: the Q tiles of the item and a ring
+// of K / V tiles.  The tensor core runs, per step and tile, O += P V of the
+// step before and S = Q K^T of this one, in this order, while the other tile's
+// softmax runs; the ring, Q and O are handed on across items, so an item's
+// epilogue overlaps the next one's first products.
+//   warps 0-3, 4-7  softmax of tile 0 / 1: a thread owns a row (TMEM lane)
+//   warp 8          TMA producer; also clears V rows behind a sequence's end
+//                   (they may hold anything; P is 0 there, but 0 x NaN is not)
+//   warp 9          MMA issuer and TMEM owner
+//
+// The softmax keeps a reference m per row; while the step's sum shows no p
+// above 2^12 the row maximum is not needed.  A larger one makes the row take
+// its maximum, and O is rescaled when that moved by more than 2^8 (rare after
+// the first step).  P is rounded to the input type for the second product (the
+// tensor core's operand type); sums, m, l and O are fp32.
+//
+// Bound by the tensor cores (two products) and by the exponentials together:
+// a 128 x 128 tile takes 1024 clocks of each at D = 128, so a share of the
+// exponentials runs on the FMA pipe (kFmaPairs).
+// Every wait is bounded; on expiry the status word reads
+// DASH_ERR_DEVICE_TIMEOUT and the roles wind down.
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "window_tc.cuh"
+
+namespace dash {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kTiles = 2;
+constexpr int kStep = 128;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+// 12 warps (10 and 11 only give their registers away): 168 registers a thread
+// at launch, 504 = 3 x 168 per warpgroup lane, redistributed as 2 x 208 + 80
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+constexpr uint32_t kColS = 0, kColO = 256;
+constexpr float kRescaleLog2 = 8.f;
+constexpr float kMaxSum = 4096.f;
+constexpr int kMaxStages = 8;
+
+template <int D>
+struct Layout {
+  static constexpr int KC = D / 64;
+  static constexpr int kChunk = 128 * 128;
+  static constexpr int kTile = KC * kChunk;
+  static constexpr int kStages = D == 128 ? 5 : 8;  // K and V tiles in flight
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = kTiles * kTile;
+  static constexpr int kOffBar = kOffKV + kStages * kTile;
+  static constexpr int kAlloc = kOffBar + 512 + 1024;
+  // of every 8 pairs of exponentials, how many take the FMA pipe
+  static constexpr int kFmaPairs = 2;
+};
+
+struct Bars {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t tail;  // a V tile with rows to clear has landed
+  uint64_t s_full[kTiles], p_full[kTiles], o_full[kTiles], o_empty[kTiles];
+  uint64_t drained;
+  uint32_t tmem_base;
+};
+
+struct Item {
+  int b, g, pos0, n, steps;
+  KeyTiles kt;
+  __device__ Item(const WindowParams& p, int P, int n_pairs, int it)
+      : b(it / (n_pairs * p.Hkv)),
+        g(it / n_pairs % p.Hkv),
+        pos0((n_pairs - 1 - it % n_pairs) * kTiles * P),  // the longest rows of a causal prompt first
+        n(window_len(p, b)),
+        kt(pos0, min(pos0 + kTiles * P, n), p.window, p.sinks, kStep) {
+    steps = pos0 < n ? kt.n : 0;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const WindowParams p, int n_pairs, int n_items) {
+  using L = Layout<D>;
+  constexpr int kStages = L::kStages;
+  constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kIdescS = tc::idesc_f16(kRows, kStep, kBF16, false, false);
+  constexpr uint32_t kIdescO = tc::idesc_f16(kRows, D, kBF16, false, true);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = kRows / p.G;
+
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->q_full, 1);
+    tc::mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&bars->kv_full[s], 1);
+      tc::mbar_init(&bars->kv_empty[s], 1);
+    }
+    tc::mbar_init(&bars->tail, 1);
+    for (int t = 0; t < kTiles; ++t) {
+      tc::mbar_init(&bars->s_full[t], 1);
+      tc::mbar_init(&bars->p_full[t], kRows);
+      tc::mbar_init(&bars->o_full[t], 1);
+      tc::mbar_init(&bars->o_empty[t], kRows);
+    }
+    tc::mbar_init(&bars->drained, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&bars->tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    tc::prefetch_tensormap(&tm_q);
+    tc::prefetch_tensormap(&tm_k);
+    tc::prefetch_tensormap(&tm_v);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  bool ok = true;
+  if (warp >= 4 * kTiles) {
+    tc::reg_dec<kOtherRegs>();
+    if (warp == kProducerWarp) {
+      // ------------------------------------------------------------ producer
+      int kv = 0, items = 0, tails = 0;  // ring slots filled, items with steps, cleared tiles
+      for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
+        const Item w(p, P, n_pairs, it);
+        if (w.steps == 0) continue;
+        if (items > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->q_empty, (items - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(&bars->q_full, kTiles * L::kTile);
+          for (int t = 0; t < kTiles; ++t)
+            for (int kc = 0; kc < L::KC; ++kc)
+              tc::tma_load_4d(smem + L::kOffQ + t * L::kTile + kc * L::kChunk, &tm_q, &bars->q_full, kc * 64, w.g * p.G,
+                              w.pos0 + t * P, w.b);
+        }
+        ++items;
+        for (int x = 0; x < 2 * w.steps; ++x, ++kv) {  // K and V of each step
+          const int st = kv % kStages, tok0 = w.kt.tile(x >> 1) * kStep;
+          if (kv >= kStages) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->kv_empty[st], ((kv / kStages) - 1) & 1));
+          if (!ok) break;
+          uint8_t* dst = smem + L::kOffKV + st * L::kTile;
+          const bool is_v = x & 1;
+          const bool clear = is_v && tok0 + kStep > w.n && w.n < p.S;
+          uint64_t* bar = clear ? &bars->tail : &bars->kv_full[st];
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(bar, L::kTile);
+            for (int kc = 0; kc < L::KC; ++kc)
+              tc::tma_load_4d(dst + kc * L::kChunk, is_v ? &tm_v : &tm_k, bar, kc * 64, w.g, tok0, w.b);
+          }
+          if (clear) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->tail, tails & 1));
+            ++tails;
+            zero_tile_rows(dst, L::KC, kStep, w.n - tok0, lane);
+            if (lane == 0) tc::mbar_arrive(&bars->kv_full[st]);
+            if (!ok) {
+              ++kv;
+              break;
+            }
+          }
+        }
+      }
+      // every copy lands before the CTA retires
+      if (items > 0) tc::mbar_wait(&bars->q_full, (items - 1) & 1);
+      for (int j = max(0, kv - kStages); j < kv; ++j) tc::mbar_wait(&bars->kv_full[j % kStages], (j / kStages) & 1);
+      if (!ok) raise_status(p.status, 5 /* DASH_ERR_DEVICE_TIMEOUT */, 321);
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      auto wait = [&](uint64_t* bar, int phase) {
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bar, phase & 1));
+        tc::fence_after_sync();
+        return ok;
+      };
+      const uint64_t q0 = tc::smem_desc_sw128(smem + L::kOffQ, 16, 1024);
+      const uint64_t k0 = tc::smem_desc_sw128(smem + L::kOffKV, 16, 1024);
+      const uint64_t v0 = tc::smem_desc_sw128(smem + L::kOffKV, L::kChunk, 1024);
+      int kv = 0, items = 0, step = 0;  // as the producer counts; steps of earlier items
+      for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
+        const Item w(p, P, n_pairs, it);
+        if (w.steps == 0) continue;
+        if (!wait(&bars->q_full, items)) break;
+        // O(t) += P(t) V of the item's step j
+        auto issue_pv = [&](int t, int j) {
+          if (j == 0 && items > 0 && !wait(&bars->o_empty[t], items - 1)) return;
+          const int x = kv + 2 * j + 1;
+          if (t == 0 && !wait(&bars->kv_full[x % kStages], x / kStages)) return;
+          if (!wait(&bars->p_full[t], step + j)) return;
+          const uint64_t vd = v0 + (uint64_t)(((x % kStages) * L::kTile) >> 4);
+          const uint32_t d_tm = tmem + kColO + t * 128, a_tm = tmem + kColS + t * 128;
+  #pragma unroll
+          for (int k = 0; k < kStep / 16; ++k)
+            tc::mma_f16_ts_w(d_tm, a_tm + k * 8, vd + (uint64_t)((k * 2048) >> 4), kIdescO, (j > 0 || k > 0) ? 1u : 0u);
+          if (t == kTiles - 1) tc::mma_commit_w(&bars->kv_empty[x % kStages]);
+        };
+        for (int i = 0; ok && i < w.steps; ++i) {
+          const int x = kv + 2 * i;
+          if (!wait(&bars->kv_full[x % kStages], x / kStages)) break;
+          const uint64_t kd = k0 + (uint64_t)(((x % kStages) * L::kTile) >> 4);
+  #pragma unroll 1
+          for (int t = 0; t < kTiles; ++t) {
+            if (i > 0) issue_pv(t, i - 1);
+            if (!ok) break;
+            const uint64_t qd = q0 + (uint64_t)((t * L::kTile) >> 4);
+  #pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = (uint64_t)((((k >> 2) * L::kChunk) + (k & 3) * 32) >> 4);
+              tc::mma_f16_ss_w(tmem + kColS + t * 128, qd + off, kd + off, kIdescS, k > 0 ? 1u : 0u);
+            }
+            tc::mma_commit_w(&bars->s_full[t]);
+          }
+          if (ok) tc::mma_commit_w(&bars->kv_empty[x % kStages]);
+        }
+        if (!ok) break;
+        tc::mma_commit_w(&bars->q_empty);
+        for (int t = 0; ok && t < kTiles; ++t) {
+          issue_pv(t, w.steps - 1);
+          if (ok) tc::mma_commit_w(&bars->o_full[t]);
+        }
+        kv += 2 * w.steps;
+        step += w.steps;
+        ++items;
+      }
+      if (!ok) raise_status(p.status, 5, 322);
+      tc::mma_commit_w(&bars->drained);
+      tc::mbar_wait(&bars->drained, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    tc::reg_inc<kSoftmaxRegs>();
+    const int t = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+    const uint32_t tb_s = tmem + ((uint32_t)(q4 * 32) << 16) + kColS + t * 128;
+    const uint32_t tb_o = tmem + ((uint32_t)(q4 * 32) << 16) + kColO + t * 128;
+    const float qk_scale = rsqrtf((float)D) * kLog2e;
+    int items = 0, step = 0;
+    for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
+      const Item w(p, P, n_pairs, it);
+      const int pos = w.pos0 + t * P + r / p.G, head = w.g * p.G + r % p.G;
+      const int lo = pos - p.window + 1;  // first key of the row's window
+      const int pos_a = w.pos0 + t * P, lo_b = pos_a + P - p.window;  // the tile's first position, its last row's lo
+      float m_used = kNegInf, lsum = 0.f;
+      for (int i = 0; i < w.steps; ++i) {
+        const int tok0 = w.kt.tile(i) * kStep;
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[t], (step + i) & 1)))) break;
+        tc::fence_after_sync();
+        uint32_t sv[kStep];
+#pragma unroll
+        for (int c = 0; c < kStep / 32; ++c) tc::tmem_ld32(tb_s + c * 32, sv + c * 32);
+        tc::tmem_wait_ld();
+        const bool edge = tok0 + kStep - 1 > pos_a || tok0 < lo_b;
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < kStep / 32; ++c) {
+            const int t0 = tok0 + c * 32;
+            const uint32_t seen = bit_range(lo - t0, pos - t0) | bit_range(0, min(pos, p.sinks - 1) - t0);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(seen & (1u << j))) sv[c * 32 + j] = __float_as_uint(kNegInf);
+          }
+        }
+        // p = 2^(s scale + off) into tensor memory; their sum
+        auto exps = [&](float off, auto all_unit) -> float {
+          const float2 sc2 = make_float2(qk_scale, qk_scale), off2 = make_float2(off, off);
+          float2 sum[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < kStep / 32; ++c) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int e = c * 32 + 2 * j;
+              const float2 y =
+                  __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sc2, off2);
+              float2 x;
+              if (!decltype(all_unit)::value && (j & 7) < L::kFmaPairs)
+                x = ex2_fma2(y);
+              else
+                x = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+              sum[j & 3] = __fadd2_rn(sum[j & 3], x);
+              pw[j] = pack2<T>(x.x, x.y);
+            }
+            tc::tmem_st16(tb_s + c * 16, pw);
+          }
+          const float2 s = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          return s.x + s.y;
+        };
+        // masked columns must give exact zeros (the special-function unit's
+        // 2^-inf), so edge steps do not use the polynomial
+        float corr = 1.f;
+        bool resc = false;
+        // the stores in exps are warp-wide, so the warp takes one path: the
+        // slow one when a row of it has no reference yet or left its range
+        const bool fast = __all_sync(0xffffffffu, m_used != kNegInf);
+        float lstep = 0.f;
+        if (fast) lstep = edge ? exps(-m_used, std::true_type{}) : exps(-m_used, std::false_type{});
+        if (!fast || __any_sync(0xffffffffu, !(lstep <= kMaxSum))) {
+          float mx = kNegInf;
+#pragma unroll
+          for (int j = 0; j < kStep; ++j) mx = fmaxf(mx, __uint_as_float(sv[j]));
+          mx *= qk_scale;
+          if (mx != kNegInf) {
+            if (m_used == kNegInf) {
+              m_used = mx;
+            } else if (mx > m_used + kRescaleLog2) {
+              corr = tc::ex2(m_used - mx);
+              m_used = mx;
+              resc = true;
+            }
+          }
+          lstep = exps(m_used == kNegInf ? 0.f : -m_used, std::true_type{});
+        }
+        lsum = lsum * corr + lstep;
+        if (__any_sync(0xffffffffu, resc)) {
+          // O is stable here: P V of the step before completed before this S
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tc::tmem_ld32(tb_o + cc * 32, ov);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * corr);
+            tc::tmem_st32(tb_o + cc * 32, ov);
+          }
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      // ---- the row's output and log-sum-exp
+      const bool live = pos < w.n;
+      T* dst = static_cast<T*>(const_cast<void*>(p.out.data)) + (int64_t)w.b * p.out.sb +
+               (int64_t)min(pos, p.S - 1) * p.out.ss + (int64_t)head * p.out.sh;
+      const float inv = live ? 1.f / lsum : 0.f;
+      if (w.steps > 0) {
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_full[t], items & 1)))) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t ov[32];
+          tc::tmem_ld32(tb_o + cc * 32, ov);
+          tc::tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(dst + cc * 32 + x * 8) = pack8<T>(ov + x * 8, inv);
+          }
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&bars->o_empty[t]);
+        step += w.steps;
+        ++items;
+      }
+      if (!live && pos < p.S) {
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) *reinterpret_cast<uint4*>(dst + x * 8) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (p.lse && pos < p.S)
+        p.lse[((int64_t)w.b * p.H + head) * p.S + pos] = live ? (m_used + log2f(lsum)) / kLog2e : kNegInf;
+    }
+    if (!ok) raise_status(p.status, 5, 323);
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D>
+cudaError_t run(const WindowParams& p, cudaStream_t stream) {
+  using L = Layout<D>;
+  CUtensorMap mq, mk, mv;
+  const int P = kRows / p.G;
+  if (!make_map(&mq, p.q, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
+      !make_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kStep) ||
+      !make_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kStep))
+    return cudaErrorInvalidValue;
+  auto kern = window_fwd_tc_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int64_t n_pairs = (p.S + kTiles * P - 1) / (kTiles * P), n_items = n_pairs * p.Hkv * p.B;
+  if (n_items > 0x7fffffff - 4096) return cudaErrorInvalidValue;
+  kern<<<(unsigned)std::min<int64_t>(n_items, p.num_sms), kThreads, L::kAlloc, stream>>>(mq, mk, mv, p, (int)n_pairs,
+                                                                                         (int)n_items);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_tc(const WindowParams& p, cudaStream_t stream) {
+  if (p.D == 128) return p.dtype == 1 ? run<__half, 128>(p, stream) : run<__nv_bfloat16, 128>(p, stream);
+  return p.dtype == 1 ? run<__half, 64>(p, stream) : run<__nv_bfloat16, 64>(p, stream);
+}
+
+}  // namespace dash
