@@ -1370,18 +1370,42 @@ dash_status_t check_window_qk(const dash_tensor_t* q, const dash_tensor_t* k) {
   return DASH_OK;
 }
 
+// window and sinks as the kernels take them: a window that hides nothing is S
+void window_extent(int64_t s, int64_t* window, int64_t* sinks) {
+  const bool all = *window == 0 || *window >= s;
+  *window = all ? s : *window;
+  *sinks = all ? 0 : std::min(*sinks, s);
+}
+
 struct WindowLayout {
-  size_t status, dd, total;
+  size_t status, dd, lse2, part, total;
+  int64_t n_tiles, n_chunks, chunk_tiles;
 };
 WindowLayout window_layout(const dash_tensor_t* q, const dash_tensor_t* k, int64_t window, int64_t sinks, bool bwd) {
   WindowLayout L{};
-  (void)k;
-  (void)window;
-  (void)sinks;
   L.status = 0;
   L.dd = align256(sizeof(dash::DeviceStatus));
   L.total = L.dd;
-  if (bwd) L.total = align256(L.dd + (size_t)q->b * q->h * q->s * 4);
+  if (!bwd) return L;
+  if (q->dtype == DASH_F32) {
+    L.total = align256(L.dd + (size_t)q->b * q->h * q->s * 4);
+    return L;
+  }
+  window_extent(q->s, &window, &sinks);
+  const int64_t pos = 128 / (q->h / k->h);  // positions of a row tile
+  L.n_tiles = (q->s + pos - 1) / pos;
+  const size_t rows = (size_t)q->b * k->h * L.n_tiles * 128 * 4;
+  L.lse2 = align256(L.dd + rows);
+  L.part = align256(L.lse2 + rows);
+  L.total = L.part;
+  if (sinks > 0) {
+    // row tiles past the band of the first 128 keys: chunks of an ordinary
+    // item's length (32 tiles at least, 64 chunks at most)
+    const int64_t far = L.n_tiles - (std::min(q->s - 1, 128 + window - 2) / pos + 1);
+    L.chunk_tiles = std::max<int64_t>({32, (window + 128) / pos, (far + 63) / 64});
+    L.n_chunks = far > 0 ? (far + L.chunk_tiles - 1) / L.chunk_tiles : 0;
+    if (L.n_chunks > 0) L.total = align256(L.part + (size_t)q->b * k->h * (L.n_chunks + 1) * 2 * 128 * q->d * 4);
+  }
   return L;
 }
 
@@ -1400,9 +1424,9 @@ dash::WindowParams window_params(const dash_tensor_t* q, const dash_tensor_t* k,
   p.Hkv = (int)k->h;
   p.G = (int)(q->h / k->h);
   p.D = (int)q->d;
-  const bool all = window == 0 || window >= q->s;
-  p.window = all ? p.S : (int)window;
-  p.sinks = all ? 0 : (int)std::min(sinks, q->s);
+  window_extent(q->s, &window, &sinks);
+  p.window = (int)window;
+  p.sinks = (int)sinks;
   p.seqlens = seqlens;
   p.lse = lse;
   p.num_sms = num_sms();
@@ -1463,8 +1487,13 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
   p.dk = solid_view(dk);
   p.dv = solid_view(dv);
   p.dd = at<float>(workspace, L.dd);
+  p.lse2 = at<float>(workspace, L.lse2);
+  p.part = at<float>(workspace, L.part);
+  p.n_tiles = (int)L.n_tiles;
+  p.n_chunks = (int)L.n_chunks;
+  p.chunk_tiles = (int)L.chunk_tiles;
   p.status = at<dash::DeviceStatus>(workspace, L.status);
-  e = dash::launch_window_bwd_simt(p, s);
+  e = q->dtype == DASH_F32 ? dash::launch_window_bwd_simt(p, s) : dash::launch_window_bwd_tc(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "window backward");
   return ok();
 }

@@ -22,9 +22,14 @@ struct WindowParams {
   int window, sinks;
   const int32_t* seqlens;   // [B] or null: rows and keys from seqlens[b] on are not there
   float* lse;               // [B, H, S] natural log-sum-exp of the row's logits, or null
-  float* dd;                // [B, H, S] dout . out (backward)
-  float* part;              // sink partials (backward, tensor-core path)
-  int n_chunks;             // query chunks of the sink keys (backward, tensor-core path)
+  float* dd;                // dout . out: [B, H, S] (backward, CUDA-core path)
+  // backward, tensor-core path, in the order of the row tiles (128 / G
+  // positions x G heads): [B, Hkv, n_tiles, 128]
+  float* lse2;              // lse in log2 units; inf on rows that are not there
+  int n_tiles;
+  float* part;              // partial dk, dv of the first 128 keys [B, Hkv, n_chunks + 1, 2, 128, D]
+  int n_chunks;             // items of chunk_tiles row tiles that see only sinks of the first 128 keys
+  int chunk_tiles;
   int num_sms;
   DeviceStatus* status;
 };
@@ -53,6 +58,7 @@ __device__ __forceinline__ int window_len(const WindowParams& p, int b) {
 
 // f16 / bf16 tensor-core path
 cudaError_t launch_window_fwd_tc(const WindowParams& p, cudaStream_t stream);
+cudaError_t launch_window_bwd_tc(const WindowParams& p, cudaStream_t stream);
 // fp32 CUDA-core path
 cudaError_t launch_window_fwd_simt(const WindowParams& p, cudaStream_t stream);
 cudaError_t launch_window_bwd_simt(const WindowParams& p, cudaStream_t stream);

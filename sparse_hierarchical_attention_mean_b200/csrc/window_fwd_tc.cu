@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
         const Item w(p, P, n_pairs, it);
         if (w.steps == 0) continue;
-        if (items > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->q_empty, (items - 1) & 1));
+        if (items > 0) ok = warp_wait(&bars->q_empty, items - 1);
         if (!ok) break;
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(&bars->q_full, kTiles * L::kTile);
@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                               w.pos0 + t * P, w.b);
         }
         ++items;
-        for (int x = 0; x < 2 * w.steps; ++x, ++kv) {  // K and V of each step
+        for (int x = 0; ok && x < 2 * w.steps; ++x, ++kv) {  // K and V of each step
           const int st = kv % kStages, tok0 = w.kt.tile(x >> 1) * kStep;
-          if (kv >= kStages) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->kv_empty[st], ((kv / kStages) - 1) & 1));
+          if (kv >= kStages) ok = warp_wait(&bars->kv_empty[st], kv / kStages - 1);
           if (!ok) break;
           uint8_t* dst = smem + L::kOffKV + st * L::kTile;
           const bool is_v = x & 1;
@@ -172,14 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tma_load_4d(dst + kc * L::kChunk, is_v ? &tm_v : &tm_k, bar, kc * 64, w.g, tok0, w.b);
           }
           if (clear) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->tail, tails & 1));
-            ++tails;
+            ok = warp_wait(&bars->tail, tails++);
             zero_tile_rows(dst, L::KC, kStep, w.n - tok0, lane);
             if (lane == 0) tc::mbar_arrive(&bars->kv_full[st]);
-            if (!ok) {
-              ++kv;
-              break;
-            }
           }
         }
       }
@@ -190,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ MMA issuer
       auto wait = [&](uint64_t* bar, int phase) {
-        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bar, phase & 1));
+        ok = ok && warp_wait(bar, phase);
         tc::fence_after_sync();
         return ok;
       };
@@ -263,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_used = kNegInf, lsum = 0.f;
       for (int i = 0; i < w.steps; ++i) {
         const int tok0 = w.kt.tile(i) * kStep;
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[t], (step + i) & 1)))) break;
+        if (!(ok = warp_wait(&bars->s_full[t], step + i))) break;
         tc::fence_after_sync();
         uint32_t sv[kStep];
 #pragma unroll
@@ -356,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                (int64_t)min(pos, p.S - 1) * p.out.ss + (int64_t)head * p.out.sh;
       const float inv = live ? 1.f / lsum : 0.f;
       if (w.steps > 0) {
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_full[t], items & 1)))) break;
+        if (!(ok = warp_wait(&bars->o_full[t], items))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {

@@ -8,6 +8,12 @@
 
 namespace dash {
 
+// Waits for phase `phase` of a barrier (counted from 0); the answer is the
+// same for the whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, phase & 1));
+}
+
 // Bits [a, b] of a 32-bit word (a, b may lie outside it).
 __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   a = max(a, 0);
