@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -151,19 +152,20 @@ def _load() -> ctypes.CDLL:
         "dash_attn_decode_noalloc_status": (i32, [vp]),
         "dash_attn_bwd_workspace_size": (sz, [T, T, i32]),
         "dash_attn_bwd": (i32, [T, T, T, vp, T, T, f32, i32, i32, O, T, T, T, vp, vp, sz, vp]),
-        "dash_attn_window_fwd_workspace_size": (sz, [T, T]),
-        "dash_attn_window_fwd": (i32, [T, T, T, vp, i64, i64, T, vp, vp, sz, vp]),
-        "dash_attn_window_bwd_workspace_size": (sz, [T, T, i64, i64]),
-        "dash_attn_window_bwd": (i32, [T, T, T, T, vp, T, vp, i64, i64, T, T, T, vp, sz, vp]),
+        # tensor descriptors as plain pointers: the binding passes them packed (_packed)
+        "dash_attn_window_fwd_workspace_size": (sz, [vp, vp]),
+        "dash_attn_window_fwd": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+        "dash_attn_window_bwd_workspace_size": (sz, [vp, vp, i64, i64]),
+        "dash_attn_window_bwd": (i32, [vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]),
         "dash_attn_window_decode_workspace_size": (sz, [i64, i64, i64]),
-        "dash_attn_window_decode": (i32, [T, T, T, vp, i64, i64, T, vp, vp, sz, vp]),
-        "dash_attn_window_decode_paged": (i32, [T, T, T, vp, i64, vp, i64, i64, T, vp, vp, sz, vp]),
+        "dash_attn_window_decode": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+        "dash_attn_window_decode_paged": (i32, [vp, vp, vp, vp, i64, vp, i64, i64, vp, vp, vp, sz, vp]),
         "dash_attn_pages_workspace_size": (sz, [i64, i64, i64]),
         "dash_attn_pages_fork": (i32, [vp, i64, i64, vp, vp, i64, vp, vp, i64, i32, vp, sz, vp]),
         "dash_attn_pages_free": (i32, [vp, i64, i64, vp, vp, i64, vp, i64, i32, vp, sz, vp]),
         "dash_attn_pages_grow": (i32, [vp, i64, i64, vp, vp, i64, vp, i32, vp, vp, vp, sz, vp]),
         "dash_attn_pages_compact": (i32, [vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
-        "dash_attn_pages_copy": (i32, [T, i64, vp, vp, i64, vp]),
+        "dash_attn_pages_copy": (i32, [vp, i64, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -180,7 +182,9 @@ class _Lazy:
     def __getattr__(self, name):
         if _Lazy._cdll is None:
             _Lazy._cdll = _load()
-        return getattr(_Lazy._cdll, name)
+        fn = getattr(_Lazy._cdll, name)
+        setattr(self, name, fn)  # the next lookup does not come here
+        return fn
 
 
 _lib = _Lazy()
@@ -659,43 +663,80 @@ def decode_paged(q, k_pages, v_pages, block_table, seqlens, summaries, alpha: fl
 # ------------------------------------------------------------------ dense / sliding-window attention
 
 
-@contextlib.contextmanager
-def _on(first: torch.Tensor, stream, *others):
-    """Device and stream of a call: every tensor on one device, buffers allocated for the stream they are used on."""
-    if not first.is_cuda:
+class _On:
+    """Device and stream of a call: every tensor on one device, buffers allocated for the stream they are used on.
+
+    ``with _On(stream, first, ...) as handle``: the cudaStream_t to launch on.  The common case (no stream given,
+    tensors on the current device) costs a microsecond; a one-token step is bound by the host otherwise.
+    """
+
+    __slots__ = ("_dev", "_stream", "_stack")
+
+    def __init__(self, stream, first, *others):
+        dev = first.get_device()
+        if dev < 0:
+            raise ValueError("tensors must be CUDA device tensors")
+        for t in others:
+            if t is not None and t.get_device() != dev:
+                raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
+        self._dev, self._stream, self._stack = dev, stream, None
+
+    def __enter__(self):
+        if self._stream is not None or self._dev != torch.cuda.current_device():
+            self._stack = contextlib.ExitStack()
+            self._stack.enter_context(torch.cuda.device(self._dev))
+            self._stack.enter_context(torch.cuda.stream(self._stream))
+        return torch._C._cuda_getCurrentRawStream(self._dev)
+
+    def __exit__(self, *error):
+        if self._stack is not None:
+            self._stack.close()
+        return False
+
+
+_PACK = struct.Struct("=qiiqqqqqqq").pack  # dash_tensor_t
+
+
+def _packed(t: torch.Tensor) -> bytes:
+    """A dash_tensor_t as bytes, with the checks of :func:`_desc`."""
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError("expected a [B, S, H, d] tensor")
+    if not t.is_cuda:
         raise ValueError("tensors must be CUDA device tensors")
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream().cuda_stream
-    else:
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
-            yield torch.cuda.current_stream().cuda_stream
+    sb, ss, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError("the last dimension must be contiguous")
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return _PACK(t.data_ptr(), code, 0, *shape, sb, ss, sh)
 
 
 def _array(t: torch.Tensor | None, name: str, shape, dtype=torch.int32):
     """Device pointer of a contiguous array of the given shape (None: not given)."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
-def _scratch(nbytes: int, what: str, device, given: torch.Tensor | None) -> torch.Tensor:
+def _scratch(nbytes: int, what: str, device, given: torch.Tensor | None):
+    """A workspace and its size in bytes."""
     if nbytes == 0:
         raise DashError(1, f"arguments rejected by {what}: {_lib.dash_attn_last_error().decode()}")
-    if given is not None and not given.is_contiguous():
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    if not given.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return _workspace(nbytes, device, given)
+    return given, given.numel() * given.element_size()
 
 
 def window_fwd_workspace_size(q: torch.Tensor, k: torch.Tensor) -> int:
-    return _lib.dash_attn_window_fwd_workspace_size(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)))
+    return _lib.dash_attn_window_fwd_workspace_size(_packed(q), _packed(k))
 
 
 def window_fwd(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None, out=None,
@@ -705,23 +746,21 @@ def window_fwd(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor |
     window 0: every earlier token.  seqlens: optional int32 [B], the valid tokens of each sequence of a padded
     batch.  Returns out [B, S, H, d], and with ``return_lse`` the log-sum-exp [B, H, S] fp32 too.
     """
-    with _on(q, stream, k, v, seqlens, out, lse, workspace) as s:
-        qd, kd, vd = _desc(q), _desc(k), _desc(v)
+    with _On(stream, q, k, v, seqlens, out, lse, workspace) as s:
+        qd, kd = _packed(q), _packed(k)
         B, S, H, _ = q.shape
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        out = torch.empty_like(q) if out is None else out
         if return_lse and lse is None:
             lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
-        lp = _array(lse, "lse", (B, H, S), torch.float32)
-        ws = _scratch(_lib.dash_attn_window_fwd_workspace_size(ctypes.byref(qd), ctypes.byref(kd)),
-                      "dash_attn_window_fwd_workspace_size", q.device, workspace)
-        _check(_lib.dash_attn_window_fwd(ctypes.byref(qd), ctypes.byref(kd), ctypes.byref(vd),
-                                         _array(seqlens, "seqlens", (B,)), window, sinks, ctypes.byref(_desc(out)),
-                                         lp, ws.data_ptr(), ws.numel() * ws.element_size(), s))
+        ws, room = _scratch(_lib.dash_attn_window_fwd_workspace_size(qd, kd), "dash_attn_window_fwd_workspace_size",
+                            q.device, workspace)
+        _check(_lib.dash_attn_window_fwd(qd, kd, _packed(v), _array(seqlens, "seqlens", (B,)), window, sinks,
+                                         _packed(out), _array(lse, "lse", (B, H, S), torch.float32), ws.data_ptr(), room, s))
     return (out, lse) if return_lse else out
 
 
 def window_bwd_workspace_size(q: torch.Tensor, k: torch.Tensor, window: int = 0, sinks: int = 0) -> int:
-    return _lib.dash_attn_window_bwd_workspace_size(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), window, sinks)
+    return _lib.dash_attn_window_bwd_workspace_size(_packed(q), _packed(k), window, sinks)
 
 
 def window_bwd(q, k, v, out, lse, dout, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None,
@@ -731,16 +770,15 @@ def window_bwd(q, k, v, out, lse, dout, window: int = 0, sinks: int = 0, seqlens
     out, lse: those of :func:`window_fwd`.  grads: optional dict of preallocated dq / dk / dv.
     """
     g = grads or {}
-    with _on(q, stream, k, v, out, lse, dout, seqlens, workspace, *g.values()) as s:
+    with _On(stream, q, k, v, out, lse, dout, seqlens, workspace, *g.values()) as s:
         B, S, H, _ = q.shape
-        dq, dk, dv = (g[n] if n in g else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                      for n, t in (("dq", q), ("dk", k), ("dv", v)))
-        qd, kd, vd, od, dod, dqd, dkd, dvd = (ctypes.byref(_desc(t)) for t in (q, k, v, out, dout, dq, dk, dv))
-        ws = _scratch(_lib.dash_attn_window_bwd_workspace_size(qd, kd, window, sinks),
-                      "dash_attn_window_bwd_workspace_size", q.device, workspace)
-        _check(_lib.dash_attn_window_bwd(qd, kd, vd, od, _array(lse, "lse", (B, H, S), torch.float32), dod,
-                                         _array(seqlens, "seqlens", (B,)), window, sinks, dqd, dkd, dvd,
-                                         ws.data_ptr(), ws.numel() * ws.element_size(), s))
+        dq, dk, dv = (g[n] if n in g else torch.empty_like(t) for n, t in (("dq", q), ("dk", k), ("dv", v)))
+        qd, kd = _packed(q), _packed(k)
+        ws, room = _scratch(_lib.dash_attn_window_bwd_workspace_size(qd, kd, window, sinks),
+                            "dash_attn_window_bwd_workspace_size", q.device, workspace)
+        _check(_lib.dash_attn_window_bwd(qd, kd, _packed(v), _packed(out), _array(lse, "lse", (B, H, S), torch.float32),
+                                         _packed(dout), _array(seqlens, "seqlens", (B,)), window, sinks, _packed(dq),
+                                         _packed(dk), _packed(dv), ws.data_ptr(), room, s))
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -784,24 +822,24 @@ def window_decode_paged(q, k_pages, v_pages, block_table, seqlens, window: int =
 
 
 def _window_decode(q, k, v, table, seqlens, window, sinks, out, return_lse, lse, workspace, stream):
-    with _on(q, stream, k, v, table, seqlens, out, lse, workspace) as s:
-        qd, kd, vd = _desc(q), _desc(k), _desc(v)
+    with _On(stream, q, k, v, table, seqlens, out, lse, workspace) as s:
+        qd, kd, vd = _packed(q), _packed(k), _packed(v)
         B, _, H, d = q.shape
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        out = torch.empty_like(q) if out is None else out
         if return_lse and lse is None:
             lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        ws = _scratch(_lib.dash_attn_window_decode_workspace_size(H, kd.h, d),
-                      "dash_attn_window_decode_workspace_size", q.device, workspace)
-        head = (ctypes.byref(qd), ctypes.byref(kd), ctypes.byref(vd))
-        tail = (_array(seqlens, "seqlens", (B,)), window, sinks, ctypes.byref(_desc(out)),
-                _array(lse, "lse", (B, H), torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        ws, room = _scratch(_lib.dash_attn_window_decode_workspace_size(H, k.shape[2], d),
+                            "dash_attn_window_decode_workspace_size", q.device, workspace)
+        tail = (_array(seqlens, "seqlens", (B,)), window, sinks, _packed(out),
+                _array(lse, "lse", (B, H), torch.float32), ws.data_ptr(), room, s)
         if table is None:
-            _check(_lib.dash_attn_window_decode(*head, *tail))
+            _check(_lib.dash_attn_window_decode(qd, kd, vd, *tail))
         else:
             if table.dim() != 2:
                 raise ValueError("block_table must be [B, max_blocks]")
             most = table.shape[1]
-            _check(_lib.dash_attn_window_decode_paged(*head, _array(table, "block_table", (B, most)), most, *tail))
+            _check(_lib.dash_attn_window_decode_paged(qd, kd, vd, _array(table, "block_table", (B, most)), most,
+                                                      *tail))
     return (out, lse) if return_lse else out
 
 
@@ -822,28 +860,27 @@ def pages_workspace_size(batch: int, max_blocks: int, n_pages: int) -> int:
 
 
 def _pages_scratch(state, device, given):
-    ws = _scratch(_lib.dash_attn_pages_workspace_size(state[1], state[2], state[5]), "dash_attn_pages_workspace_size",
-                  device, given)
-    return ws, (ws.data_ptr(), ws.numel() * ws.element_size())
+    return _scratch(_lib.dash_attn_pages_workspace_size(state[1], state[2], state[5]),
+                    "dash_attn_pages_workspace_size", device, given)
 
 
 def pages_fork(block_table, seqlens, refs, src, dst, block: int, workspace=None, stream=None) -> None:
     """Sequences dst[i] become copies of src[i] that share their pages, in place (see dash_attn_pages_fork)."""
-    with _on(block_table, stream, seqlens, refs, src, dst, workspace) as s:
+    with _On(stream, block_table, seqlens, refs, src, dst, workspace) as s:
         state = _pages_state(block_table, seqlens, refs)
         n = dst.numel()
         ws, room = _pages_scratch(state, block_table.device, workspace)
-        _check(_lib.dash_attn_pages_fork(*state, _array(src, "src", (n,)), _array(dst, "dst", (n,)), n, block, *room,
-                                         s))
+        _check(_lib.dash_attn_pages_fork(*state, _array(src, "src", (n,)), _array(dst, "dst", (n,)), n, block, ws.data_ptr(),
+                                         room, s))
 
 
 def pages_free(block_table, seqlens, refs, slots, block: int, workspace=None, stream=None) -> None:
     """The sequences slots[i] give back their pages, in place (see dash_attn_pages_free)."""
-    with _on(block_table, stream, seqlens, refs, slots, workspace) as s:
+    with _On(stream, block_table, seqlens, refs, slots, workspace) as s:
         state = _pages_state(block_table, seqlens, refs)
         n = slots.numel()
         ws, room = _pages_scratch(state, block_table.device, workspace)
-        _check(_lib.dash_attn_pages_free(*state, _array(slots, "slots", (n,)), n, block, *room, s))
+        _check(_lib.dash_attn_pages_free(*state, _array(slots, "slots", (n,)), n, block, ws.data_ptr(), room, s))
 
 
 def pages_grow(block_table, seqlens, refs, n_new, block: int, workspace=None, stream=None):
@@ -853,14 +890,14 @@ def pages_grow(block_table, seqlens, refs, n_new, block: int, workspace=None, st
     written (-1: none).  When the pool has too few free pages nothing changes; pass a workspace to read that from
     :func:`device_status`.
     """
-    with _on(block_table, stream, seqlens, refs, n_new, workspace) as s:
+    with _On(stream, block_table, seqlens, refs, n_new, workspace) as s:
         state = _pages_state(block_table, seqlens, refs)
         batch = state[1]
-        copies = torch.empty((2, batch), dtype=torch.int32, device=block_table.device)
+        src, dst = torch.empty((2, batch), dtype=torch.int32, device=block_table.device).unbind()
         ws, room = _pages_scratch(state, block_table.device, workspace)
-        _check(_lib.dash_attn_pages_grow(*state, _array(n_new, "n_new", (batch,)), block, copies[0].data_ptr(),
-                                         copies[1].data_ptr(), *room, s))
-    return copies[0], copies[1]
+        _check(_lib.dash_attn_pages_grow(*state, _array(n_new, "n_new", (batch,)), block, src.data_ptr(),
+                                         dst.data_ptr(), ws.data_ptr(), room, s))
+    return src, dst
 
 
 def pages_compact(block_table, seqlens, refs, block: int, inplace: bool = False, workspace=None, stream=None) -> dict:
@@ -869,17 +906,16 @@ def pages_compact(block_table, seqlens, refs, block: int, inplace: bool = False,
     Returns table and refs after it (the inputs themselves with ``inplace``), the moves src, dst [n_pages // 2] to
     make with :func:`pages_copy` (-1 past their number) and info [2] = {moves, pages in use}.
     """
-    with _on(block_table, stream, seqlens, refs, workspace) as s:
+    with _On(stream, block_table, seqlens, refs, workspace) as s:
         state = _pages_state(block_table, seqlens, refs)
         dev, n_pages = block_table.device, state[5]
         table_out = block_table if inplace else torch.empty_like(block_table)
         refs_out = refs if inplace else torch.empty_like(refs)
-        moves = torch.empty((2, n_pages // 2), dtype=torch.int32, device=dev)
+        src, dst = torch.empty((2, n_pages // 2), dtype=torch.int32, device=dev).unbind()
         info = torch.empty(2, dtype=torch.int32, device=dev)
         ws, room = _pages_scratch(state, dev, workspace)
-        src, dst = moves[0], moves[1]
         _check(_lib.dash_attn_pages_compact(*state, block, table_out.data_ptr(), refs_out.data_ptr(), src.data_ptr(),
-                                            dst.data_ptr(), info.data_ptr(), *room, s))
+                                            dst.data_ptr(), info.data_ptr(), ws.data_ptr(), room, s))
     return {"table": table_out, "refs": refs_out, "src": src, "dst": dst, "info": info}
 
 
@@ -888,7 +924,7 @@ def pages_copy(pools, src, dst, stream=None) -> None:
     pools = list(pools)
     if not pools:
         raise ValueError("no pools")
-    with _on(pools[0], stream, *pools[1:], src, dst) as s:
+    with _On(stream, *pools, src, dst) as s:
         n = src.numel()
-        descs = (DashTensor * len(pools))(*[_desc(t) for t in pools])
-        _check(_lib.dash_attn_pages_copy(descs, len(pools), _array(src, "src", (n,)), _array(dst, "dst", (n,)), n, s))
+        _check(_lib.dash_attn_pages_copy(b"".join(map(_packed, pools)), len(pools), _array(src, "src", (n,)),
+                                         _array(dst, "dst", (n,)), n, s))

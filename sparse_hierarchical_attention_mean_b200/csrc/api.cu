@@ -1450,11 +1450,9 @@ dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* 
   const WindowLayout L = window_layout(q, k, window, sinks, false);
   if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(dash::DeviceStatus), s);
-  if (e != cudaSuccess) return cuda_fail(e, "memset");
   dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, lse);
   p.status = at<dash::DeviceStatus>(workspace, L.status);
-  e = q->dtype == DASH_F32 ? dash::launch_window_fwd_simt(p, s) : dash::launch_window_fwd_tc(p, s);
+  const cudaError_t e = q->dtype == DASH_F32 ? dash::launch_window_fwd_simt(p, s) : dash::launch_window_fwd_tc(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "window forward");
   return ok();
 }
@@ -1479,8 +1477,6 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
   const WindowLayout L = window_layout(q, k, window, sinks, true);
   if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(dash::DeviceStatus), s);
-  if (e != cudaSuccess) return cuda_fail(e, "memset");
   dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, const_cast<float*>(lse));
   p.dout = solid_view(dout);
   p.dq = solid_view(dq);
@@ -1493,7 +1489,7 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
   p.n_chunks = (int)L.n_chunks;
   p.chunk_tiles = (int)L.chunk_tiles;
   p.status = at<dash::DeviceStatus>(workspace, L.status);
-  e = q->dtype == DASH_F32 ? dash::launch_window_bwd_simt(p, s) : dash::launch_window_bwd_tc(p, s);
+  const cudaError_t e = q->dtype == DASH_F32 ? dash::launch_window_bwd_simt(p, s) : dash::launch_window_bwd_tc(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "window backward");
   return ok();
 }

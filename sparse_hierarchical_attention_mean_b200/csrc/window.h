@@ -48,12 +48,23 @@ struct KeyTiles {
   __host__ __device__ int tile(int i) const { return i < n_sink ? i : band0 + i - n_sink; }
 };
 
-// Valid length of sequence b (clamped to [0, S]; reported when out of range).
+// Valid length of sequence b, clamped to [0, S].
 __device__ __forceinline__ int window_len(const WindowParams& p, int b) {
-  if (!p.seqlens) return p.S;
-  const int n = p.seqlens[b];
-  if (n < 0 || n > p.S) raise_status(p.status, 1 /* DASH_ERR_INVALID_ARGUMENT */, 301);
-  return min(max(n, 0), p.S);
+  return p.seqlens ? min(max(p.seqlens[b], 0), p.S) : p.S;
+}
+
+// The call's status word, written by one warp of the first CTA of its first
+// kernel when it starts: lengths out of range, else 0.  What other CTAs report
+// later is a wait that ran out, a second or more after the kernel's start.
+__device__ __forceinline__ void begin_status(const WindowParams& p, int lane) {
+  bool bad = false;
+  if (p.seqlens)
+    for (int b = lane; b < p.B; b += 32) bad = bad || p.seqlens[b] < 0 || p.seqlens[b] > p.S;
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) {
+    p.status->code = bad ? 1 /* DASH_ERR_INVALID_ARGUMENT */ : 0;
+    p.status->detail = bad ? 301 : 0;
+  }
 }
 
 // f16 / bf16 tensor-core path

@@ -137,9 +137,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   bool ok = true;
+  // the key kernel may take the SMs that are or get free; it waits for this
+  // grid's end before it reads lse2 and D
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
+    if (blockIdx.x == 0) begin_status(p, lane);
     int kv = 0, items = 0, tails = 0;
     for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
       const RowItem w(p, P, it);
@@ -510,6 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   bool ok = true;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // the row kernel's lse2 and D; all roles wait here, so that the limits of
+  // their own waits do not run while that kernel does
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
@@ -775,6 +783,7 @@ __global__ void __launch_bounds__(256) window_bwd_join_kernel(const WindowParams
   if (key >= p.S) return;
   const float* src = p.part + (int64_t)bg * (p.n_chunks + 1) * 2 * kRows * D + i;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   for (int x = 0; x <= p.n_chunks; ++x) {
     const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)x * 2 * kRows * D);
     s.x += v.x;
@@ -788,6 +797,23 @@ __global__ void __launch_bounds__(256) window_bwd_join_kernel(const WindowParams
   T* dst = static_cast<T*>(const_cast<void*>(out.data)) + (int64_t)b * out.sb + (int64_t)key * out.ss +
            (int64_t)g * out.sh + c;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(s.x * f, s.y * f), pack2<T>(s.z * f, s.w * f));
+}
+
+// A launch that may start before the kernel in front of it ends; it waits for
+// that kernel's results itself (griddepcontrol.wait).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <typename T, int D>
@@ -822,14 +848,12 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
     auto kern = window_bwd_key_tc_kernel<T, D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
-    kern<<<(unsigned)std::min<int64_t>(key_items, p.num_sms), kThreads, L::kAlloc, stream>>>(mq, mdo, mk, mv, p,
-                                                                                             (int)key_items);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_early(kern, dim3((unsigned)std::min<int64_t>(key_items, p.num_sms)), kThreads, L::kAlloc, stream, mq,
+                          mdo, mk, mv, p, (int)key_items)) != cudaSuccess)
+      return e;
   }
-  if (p.n_chunks > 0) {
-    window_bwd_join_kernel<T, D><<<dim3(p.B * p.Hkv, 2 * kRows * D / 1024), 256, 0, stream>>>(p);
-    e = cudaGetLastError();
-  }
+  if (p.n_chunks > 0)
+    e = launch_early(window_bwd_join_kernel<T, D>, dim3(p.B * p.Hkv, 2 * kRows * D / 1024), 256, 0, stream, p);
   return e;
 }
 

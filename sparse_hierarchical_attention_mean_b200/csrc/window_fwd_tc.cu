@@ -48,7 +48,7 @@ constexpr int kRows = 128;
 constexpr int kTiles = 2;
 constexpr int kStep = 128;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
-// 12 warps (10 and 11 only give their registers away): 168 registers a thread
+// 12 warps (10 writes the status word, else 10 and 11 only give their registers away): 168 registers a thread
 // at launch, 504 = 3 x 168 per warpgroup lane, redistributed as 2 x 208 + 80
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
   if (warp >= 4 * kTiles) {
     tc::reg_dec<kOtherRegs>();
+    if (warp == kMmaWarp + 1 && blockIdx.x == 0) begin_status(p, lane);
     if (warp == kProducerWarp) {
       // ------------------------------------------------------------ producer
       int kv = 0, items = 0, tails = 0;  // ring slots filled, items with steps, cleared tiles

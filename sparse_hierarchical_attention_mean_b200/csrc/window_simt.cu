@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(WindowParams 
   float* ks = qs + tile_floats<D>();
   float* vs = ks + tile_floats<D>();
   float* ps = vs + tile_floats<D>();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 32) begin_status(p, threadIdx.x);
   const int h = blockIdx.y, b = blockIdx.z, g = h / p.G;
   const int r0 = blockIdx.x * kT;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -215,6 +216,7 @@ __global__ void __launch_bounds__(kThreads) window_bwd_row_simt_kernel(WindowPar
   float* ks = dos + tile_floats<D>();
   float* vs = ks + tile_floats<D>();
   float* dss = vs + tile_floats<D>();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 32) begin_status(p, threadIdx.x);
   const int h = blockIdx.y, b = blockIdx.z, g = h / p.G;
   const int r0 = blockIdx.x * kT;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;

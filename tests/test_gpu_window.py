@@ -5,6 +5,7 @@ and the reference takes the same one.
 """
 
 import math
+import threading
 
 import pytest
 import torch
@@ -248,6 +249,41 @@ def test_other_stream(cuda_lib):
     grads = dash.window_bwd(q, k, v, *outs[0], do, 50, 4, stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) and torch.equal(x, lse) for o, x in outs)
+    assert all(torch.equal(grads[n], wantg[n]) for n in wantg)
+
+
+def test_first_cuda_work_of_a_thread(cuda_lib):
+    """Every call works in a thread that has done no CUDA work before (as autograd's threads)."""
+    dash = cuda_lib
+    case = (1, 200, 4, 2, 64, F16, 50, 4, None)
+    q, k, v, do, _ = _inputs(case, 7)
+    want, lse = dash.window_fwd(q, k, v, 50, 4, return_lse=True)
+    wantg = dash.window_bwd(q, k, v, want, lse, do, 50, 4)
+    seqlens = torch.tensor([200], dtype=torch.int32, device="cuda")
+    q1 = q[:, -1:].contiguous()
+    want1 = dash.window_decode(q1, k, v, seqlens, 50, 4)
+    out, lse2, out1 = torch.empty_like(want), torch.empty_like(lse), torch.empty_like(want1)
+    grads = {n: torch.empty_like(t) for n, t in wantg.items()}
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    calls = [lambda: dash.window_fwd(q, k, v, 50, 4, out=out, lse=lse2, workspace=ws),
+             lambda: dash.window_bwd(q, k, v, out, lse2, do, 50, 4, grads=grads, workspace=ws),
+             lambda: dash.window_decode(q1, k, v, seqlens, 50, 4, out=out1, workspace=ws)]
+    failed = []
+
+    def run(call):
+        try:
+            call()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    for call in calls:
+        t = threading.Thread(target=run, args=(call,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    assert torch.equal(out, want) and torch.equal(lse2, lse) and torch.equal(out1, want1)
     assert all(torch.equal(grads[n], wantg[n]) for n in wantg)
 
 
