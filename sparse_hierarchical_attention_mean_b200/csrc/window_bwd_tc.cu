@@ -26,13 +26,6 @@ constexpr int kWorkers = 256;  // warps 0-7
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kTimeout = 5;  // DASH_ERR_DEVICE_TIMEOUT
 
-// 2^x of a pair, every fourth pair on the FMA pipe
-template <bool kFma>
-__device__ __forceinline__ float2 ex2_2(float2 x) {
-  if constexpr (kFma) return ex2_fma2(x);
-  return make_float2(tc::ex2(x.x), tc::ex2(x.y));
-}
-
 // ------------------------------------------------------------------ rows: dq, D
 //
 // A CTA (one per SM) walks 128-row tiles; per tile the keys its rows see come
@@ -75,10 +68,10 @@ struct RowBars {
 struct RowItem {
   int b, g, tile, pos0, n, steps;
   KeyTiles kt;
-  __device__ RowItem(const WindowParams& p, int P, int it)
-      : b(it / (p.n_tiles * p.Hkv)),
-        g(it / p.n_tiles % p.Hkv),
-        tile(p.n_tiles - 1 - it % p.n_tiles),
+  __device__ RowItem(const WindowParams& p, int P, const ItemWalk& w)
+      : b(w.b),
+        g(w.g),
+        tile(w.n_x - 1 - w.x),
         pos0(tile * P),
         n(window_len(p, b)),
         kt(pos0, min(pos0 + P, n), p.window, p.sinks, kStepR) {
@@ -90,7 +83,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_bwd_row_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                              const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_k,
-                             const __grid_constant__ CUtensorMap tm_v, const WindowParams p, int n_items) {
+                             const __grid_constant__ CUtensorMap tm_v, const WindowParams p) {
   using L = RowLayout<D>;
   constexpr int kStages = L::kStages;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
@@ -101,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   RowBars* bars = reinterpret_cast<RowBars*>(smem + L::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = kRows / p.G;
+  const int lg = __ffs(p.G) - 1, P = kRows >> lg;
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->rows_full, 1);
@@ -145,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     if (blockIdx.x == 0) begin_status(p, lane);
     int kv = 0, items = 0, tails = 0;
-    for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
+    for (ItemWalk it(p.n_tiles, p.Hkv, p.B); ok && it.any(); it.next()) {
       const RowItem w(p, P, it);
       if (w.steps == 0) continue;
       if (items > 0) ok = warp_wait(&bars->rows_empty, items - 1);
@@ -197,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t v0 = tc::smem_desc_sw128(smem + L::kOffKV + L::kKeyTile, 16, 1024);
     const uint64_t kmn0 = tc::smem_desc_sw128(smem + L::kOffKV, L::kKeyChunk, 1024);
     int kv = 0, items = 0;
-    for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
+    for (ItemWalk it(p.n_tiles, p.Hkv, p.B); ok && it.any(); it.next()) {
       const RowItem w(p, P, it);
       if (w.steps == 0) continue;
       if (!wait(&bars->ready, items)) break;
@@ -250,11 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // the first item with steps from `it` on; tiles behind the sequence's end
     // get dq = 0 and lse2 = inf (p = 0) on the way
-    auto seek = [&](int it) {
-      for (; it < n_items; it += gridDim.x) {
+    auto seek = [&](ItemWalk& it) {
+      for (; it.any(); it.next()) {
         const RowItem w(p, P, it);
         if (w.steps > 0) break;
-        const int pos = w.pos0 + r / p.G, head = w.g * p.G + r % p.G;
+        const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
         if (wg == 0) {
           const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
           p.lse2[at] = -kNegInf;
@@ -266,12 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < D / 8; ++x) *reinterpret_cast<uint4*>(dst + x * 8) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      return it;
     };
     // Q (warps 0-3) and dout (4-7) into TMEM, D = dout . out and lse2
-    auto load_rows = [&](int it) {
+    auto load_rows = [&](const ItemWalk& it) {
       const RowItem w(p, P, it);
-      const int pos = w.pos0 + r / p.G, head = w.g * p.G + r % p.G;
+      const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
       const bool live = pos < w.n;
       lse2 = live ? p.lse[((int64_t)w.b * p.H + head) * p.S + pos] * kLog2e : -kNegInf;
       if (!warp_wait(&bars->rows_full, items)) return false;
@@ -308,11 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
 
-    int it = seek(blockIdx.x);
-    if (it < n_items) ok = load_rows(it);
-    while (ok && it < n_items) {
+    ItemWalk it(p.n_tiles, p.Hkv, p.B);
+    seek(it);
+    if (it.any()) ok = load_rows(it);
+    while (ok && it.any()) {
       const RowItem w(p, P, it);
-      const int pos = w.pos0 + r / p.G, head = w.g * p.G + r % p.G;
+      const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
       const int lo = pos - p.window + 1;
       const int lo_b = w.pos0 + P - p.window;  // the last row's lo
       for (int i = (step & 1) == wg ? 0 : 1; i < w.steps; i += 2) {
@@ -357,8 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || !(ok = warp_wait(&bars->dq_full, items))) break;
       tc::fence_after_sync();
       ++items;
-      const int next = seek(it + gridDim.x);
-      if (next < n_items && !(ok = load_rows(next))) break;
+      it.next();
+      seek(it);
+      if (it.any() && !(ok = load_rows(it))) break;
       // ---- dq of this item, each group half of the columns
       T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb +
                (int64_t)min(pos, p.S - 1) * p.dq.ss + (int64_t)head * p.dq.sh;
@@ -380,7 +374,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_before_sync();
       tc::mbar_arrive(&bars->dq_empty);
-      it = next;
     }
     if (!ok) raise_status(p.status, kTimeout, 333);
   }
@@ -438,29 +431,20 @@ struct KeyBars {
 
 struct KeyItem {
   int b, g, k0, slot, n, t0, t1;  // keys from k0; partial slot, -1: final; row tiles [t0, t1)
-  __device__ KeyItem(const WindowParams& p, int P, int it) {
-    // the band's row tiles of key tile 0 end before first_far (chunks follow)
-    const int chunk_items = p.n_chunks * p.Hkv * p.B;
-    const int first_far = min(p.S - 1, kRows + p.window - 2) / P + 1;
-    if (it < chunk_items) {
-      const int c = it % p.n_chunks, bg = it / p.n_chunks;
-      b = bg / p.Hkv;
-      g = bg % p.Hkv;
-      n = window_len(p, b);
+  __device__ KeyItem(const WindowParams& p, int lgp, const ItemWalk& w) : b(w.b), g(w.g), n(window_len(p, b)) {
+    if (w.x < p.n_chunks) {
+      // the band's row tiles of key tile 0 end before these
+      const int first_far = (min(p.S - 1, kRows + p.window - 2) >> lgp) + 1;
       k0 = 0;
-      slot = 1 + c;
-      t0 = first_far + c * p.chunk_tiles;
-      t1 = min(t0 + p.chunk_tiles, (n + P - 1) / P);
+      slot = 1 + w.x;
+      t0 = first_far + w.x * p.chunk_tiles;
+      t1 = min(t0 + p.chunk_tiles, (n + (1 << lgp) - 1) >> lgp);
     } else {
-      const int x = it - chunk_items, key_tiles = (p.S + kRows - 1) / kRows, bg = x / key_tiles;
-      b = bg / p.Hkv;
-      g = bg % p.Hkv;
-      n = window_len(p, b);
-      k0 = x % key_tiles * kRows;
+      k0 = (w.x - p.n_chunks) * kRows;
       slot = k0 == 0 && p.n_chunks > 0 ? 0 : -1;
-      t0 = k0 / P;
+      t0 = k0 >> lgp;
       // the last row that sees a key of the tile
-      t1 = k0 < n ? (int)min((int64_t)n - 1, (int64_t)k0 + kRows - 1 + p.window - 1) / P + 1 : t0;
+      t1 = k0 < n ? ((int)min((int64_t)n - 1, (int64_t)k0 + kRows - 1 + p.window - 1) >> lgp) + 1 : t0;
     }
     t1 = max(t1, t0);
   }
@@ -470,7 +454,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_bwd_key_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                             const WindowParams p, int n_items) {
+                             const WindowParams p, int n_x) {
   using L = KeyLayout<D>;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kIdescS = tc::idesc_f16(kRows, kRows, kBF16, false, false);
@@ -480,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   KeyBars* bars = reinterpret_cast<KeyBars*>(smem + L::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = kRows / p.G;
+  const int lgp = 8 - __ffs(p.G), P = 1 << lgp;  // positions of a row tile
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->kv_full, 1);
@@ -522,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     int q = 0, items = 0, tails = 0;
-    for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
-      const KeyItem w(p, P, it);
+    for (ItemWalk it(n_x, p.Hkv, p.B); ok && it.any(); it.next()) {
+      const KeyItem w(p, lgp, it);
       if (w.t0 == w.t1) continue;
       if (items > 0) ok = warp_wait(&bars->kv_empty, items - 1);
       if (!ok) break;
@@ -597,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const uint64_t tile16 = (uint64_t)(L::kTile >> 4);
     int q = 0, items = 0;
-    for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
-      const KeyItem w(p, P, it);
+    for (ItemWalk it(n_x, p.Hkv, p.B); ok && it.any(); it.next()) {
+      const KeyItem w(p, lgp, it);
       if (w.t0 == w.t1) continue;
       const int n = w.t1 - w.t0;
       if (!wait(&bars->kv_full, items) || !wait(&bars->q_full[q % kNS], q / kNS)) break;
@@ -634,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tb = tmem + ((uint32_t)(q4 * 32) << 16);
     const float sc = rsqrtf((float)D) * kLog2e;
     int q = 0, items = 0;
-    for (int it = blockIdx.x; ok && it < n_items; it += gridDim.x) {
-      const KeyItem w(p, P, it);
+    for (ItemWalk it(n_x, p.Hkv, p.B); ok && it.any(); it.next()) {
+      const KeyItem w(p, lgp, it);
       const int key = w.k0 + k;
       for (int t = w.t0; t < w.t1; ++t, ++q) {
         const int st = q % kNS, pos0 = t * P;
@@ -657,12 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       make_float2(-l4.x, -l4.y));
           const float2 b = __ffma2_rn(make_float2(__uint_as_float(pf[j + 2]), __uint_as_float(pf[j + 3])), sc2,
                                       make_float2(-l4.z, -l4.w));
-          const float2 ea = ex2_2<false>(a);
-          const float2 eb = (j & 4) ? ex2_2<true>(b) : ex2_2<false>(b);
-          pf[j] = __float_as_uint(ea.x);
-          pf[j + 1] = __float_as_uint(ea.y);
-          pf[j + 2] = __float_as_uint(eb.x);
-          pf[j + 3] = __float_as_uint(eb.y);
+          pf[j] = __float_as_uint(tc::ex2(a.x));
+          pf[j + 1] = __float_as_uint(tc::ex2(a.y));
+          pf[j + 2] = __float_as_uint(tc::ex2(b.x));
+          pf[j + 3] = __float_as_uint(tc::ex2(b.y));
         }
         if (edge) {
           // rows from the key's own on, to the last whose window holds it
@@ -836,8 +818,7 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
     auto kern = window_bwd_row_tc_kernel<T, D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
-    kern<<<(unsigned)std::min<int64_t>(row_items, p.num_sms), kThreads, L::kAlloc, stream>>>(mq, mdo, mo, mk, mv, p,
-                                                                                             (int)row_items);
+    kern<<<(unsigned)std::min<int64_t>(row_items, p.num_sms), kThreads, L::kAlloc, stream>>>(mq, mdo, mo, mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   {
@@ -849,7 +830,7 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
     if ((e = launch_early(kern, dim3((unsigned)std::min<int64_t>(key_items, p.num_sms)), kThreads, L::kAlloc, stream, mq,
-                          mdo, mk, mv, p, (int)key_items)) != cudaSuccess)
+                          mdo, mk, mv, p, (p.S + kRows - 1) / kRows + p.n_chunks)) != cudaSuccess)
       return e;
   }
   if (p.n_chunks > 0)

@@ -1,6 +1,7 @@
-// Device helpers of the tensor-core sliding-window kernels: visibility masks
-// and 2^x on the FMA pipe.
+// Device helpers of the tensor-core sliding-window kernels.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "tc.cuh"
@@ -14,6 +15,33 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase) {
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, phase & 1));
 }
 
+// A CTA's work items x of (n_x per head, Hkv, B), x fastest: every gridDim.x-th
+// from blockIdx.x on.  The steps between them are kept as digits, so that the
+// way to the next item takes no division.
+struct ItemWalk {
+  int x, g, b, n_x, n_g, n_b, dx, dg, db;
+  __device__ ItemWalk(int n_x, int n_g, int n_b) : n_x(n_x), n_g(n_g), n_b(n_b) {
+    split(blockIdx.x, &x, &g, &b);
+    split(gridDim.x, &dx, &dg, &db);
+  }
+  __device__ void split(int i, int* x, int* g, int* b) const {
+    *x = i % n_x;
+    i /= n_x;
+    *g = i % n_g;
+    *b = i / n_g;
+  }
+  __device__ bool any() const { return b < n_b; }
+  __device__ void next() {
+    x += dx;
+    const bool c = x >= n_x;
+    x -= c ? n_x : 0;
+    g += dg + c;
+    const bool c2 = g >= n_g;
+    g -= c2 ? n_g : 0;
+    b += db + c2;
+  }
+};
+
 // Bits [a, b] of a 32-bit word (a, b may lie outside it).
 __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   a = max(a, 0);
@@ -21,31 +49,23 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   return a > b ? 0u : (0xffffffffu << a) & (0xffffffffu >> (31 - b));
 }
 
-// 2^x of a pair without the special-function unit: x = k + f with k the
-// nearest integer (added and taken off again in the units of 1.5 * 2^23), f in
-// [-1/2, 1/2], 2^f by a polynomial and k added to its exponent (the range
-// reduction of Cody & Waite, Software Manual for the Elementary Functions).
-// The coefficients are the degree-4 minimax polynomial of the relative error
-// on [-1/2, 1/2] (Remez exchange): 2.6e-6.  x is taken as at least -125: the
-// value below that, 2^-125, is zero for every use here.
-//
-// The unit computes 16 of these a clock and SM, 1/64 of the FMAs that a
-// 128 x 128 score tile leaves unused, so the softmax sends part of its
-// exponentials here.
-__device__ __forceinline__ float2 ex2_fma2(float2 x) {
-  x.x = fmaxf(x.x, -125.f);
-  x.y = fmaxf(x.y, -125.f);
-  const float2 big = make_float2(12582912.f, 12582912.f), nbig = make_float2(-12582912.f, -12582912.f);
-  const float2 r = __fadd2_rn(x, big);
-  const float2 k = __fadd2_rn(r, nbig);
-  const float2 f = __ffma2_rn(k, make_float2(-1.f, -1.f), x);
-  float2 p = make_float2(9.570101911e-03f, 9.570101911e-03f);
-  p = __ffma2_rn(p, f, make_float2(5.591786032e-02f, 5.591786032e-02f));
-  p = __ffma2_rn(p, f, make_float2(2.402474483e-01f, 2.402474483e-01f));
-  p = __ffma2_rn(p, f, make_float2(6.931218147e-01f, 6.931218147e-01f));
-  p = __ffma2_rn(p, f, make_float2(9.999992614e-01f, 9.999992614e-01f));
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(r.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(r.y) << 23)));
+// 2^x and the packing of a pair (the first in the low half) that keep their
+// place in the instruction stream: a warp issues in order, so the softmax
+// interleaves the special-function unit's instructions (8 clocks each) with
+// the FMAs, sums and conversions of other elements by hand.
+__device__ __forceinline__ float ex2_placed(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_placed(float2 x) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile("cvt.rn.bf16x2.f32 %0, %2, %1;\n" : "=r"(r) : "f"(x.x), "f"(x.y));
+  else
+    asm volatile("cvt.rn.f16x2.f32 %0, %2, %1;\n" : "=r"(r) : "f"(x.x), "f"(x.y));
+  return r;
 }
 
 // 16-byte stores of 8 values rounded to T.
@@ -57,6 +77,29 @@ __device__ __forceinline__ uint4 pack8(const uint32_t* v, float scale) {
   w.z = pack2<T>(__uint_as_float(v[4]) * scale, __uint_as_float(v[5]) * scale);
   w.w = pack2<T>(__uint_as_float(v[6]) * scale, __uint_as_float(v[7]) * scale);
   return w;
+}
+
+// Rows to columns in groups of eight lanes: before, lane r of a group holds the
+// eight 16-byte pieces of its row; after, lane c holds piece c of the group's
+// rows in v[0..7].  A warp's store of v[i] then writes four rows of 128
+// contiguous bytes instead of 32 rows of 16 (four lines instead of 32).
+__device__ __forceinline__ void transpose8(uint4 (&v)[8], int lane) {
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i & d) continue;
+      const uint4 a = v[i], b = v[i | d];
+      uint4 x = up ? a : b;
+      x.x = __shfl_xor_sync(0xffffffffu, x.x, d);
+      x.y = __shfl_xor_sync(0xffffffffu, x.y, d);
+      x.z = __shfl_xor_sync(0xffffffffu, x.z, d);
+      x.w = __shfl_xor_sync(0xffffffffu, x.w, d);
+      v[i] = up ? x : a;
+      v[i | d] = up ? b : x;
+    }
+  }
 }
 
 // Zeroes rows [row0, rows) of a tile of 64-column chunks ([rows][128 bytes]
