@@ -29,37 +29,40 @@ constexpr int kTimeout = 5;  // DASH_ERR_DEVICE_TIMEOUT
 // ------------------------------------------------------------------ rows: dq, D
 //
 // A CTA (one per SM) walks 128-row tiles; per tile the keys its rows see come
-// in steps of 64 (sink steps before the band, then the band).
-//   S = Q K^T, dP = dout V^T   A = Q, dout from TMEM; two buffers
-//   dS over S in 16 bits;  dQ += dS K  (A from TMEM, K MN-major)
-// Warps 0-3 take the even steps, 4-7 the odd ones: while one group forms dS,
-// the tensor core works for the other.  The next tile's Q, dout and out come
-// by TMA during this one, and are moved to TMEM (with D) before this tile's dq
-// is written, so its first products overlap that.  Warp 8 is the TMA
-// producer, which also clears K rows behind a sequence's end; warp 9 issues
-// the MMAs.  TMEM: Q at 0, dout at D / 2, buffers at 128 + 128 b (S, dP), dQ
-// at 384.
-constexpr int kStepR = 64;
-constexpr uint32_t kColBuf = 128, kColDQ = 384;
+// in steps of 128 (at most one step of sinks before the band, then the band).
+//   S = Q K^T, dP = dout V^T   A = Q, dout from TMEM
+//   dS over dP in 16 bits;  dQ += dS K  (A from TMEM, K MN-major)
+// Warps 0-7 are the workers (two per TMEM lane quarter, 64 keys each).  S of
+// the next step runs as soon as S is in their registers, dP of the next step
+// behind dQ of this one, so that the tensor core works while they do.  The next
+// tile's Q, dout and out come by TMA during this one (out through the ring);
+// D is formed while the last dQ runs, Q and dout are moved to TMEM before this
+// tile's dq is written, so the next tile's first products overlap that.  Warp 8
+// is the TMA producer, which also clears K rows behind a sequence's end; warp 9
+// issues the MMAs.  TMEM: Q at 0, dout at D / 2, S, dP, dQ at 128, 256, 384.
+// (Steps of 64 keys in two buffers were slower: a 128 x 64 product takes the
+// tensor core 55 clocks, not 32, and S, dP and dQ of 64 keys 1100.)
+constexpr uint32_t kColSR = 128, kColDPR = 256, kColDQ = 384;
 
 template <int D>
 struct RowLayout {
   static constexpr int KC = D / 64;
-  static constexpr int kRowChunk = kRows * 128, kRowTile = KC * kRowChunk;
-  static constexpr int kKeyChunk = kStepR * 128, kKeyTile = KC * kKeyChunk;
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kOffQ = 0, kOffDo = kRowTile, kOffO = 2 * kRowTile;
-  static constexpr int kOffKV = 3 * kRowTile;  // [kStages] K, V
-  static constexpr int kOffBar = kOffKV + kStages * 2 * kKeyTile;
-  static constexpr int kAlloc = kOffBar + 512 + 1024;
+  static constexpr int kChunk = 128 * 128, kTile = KC * kChunk;
+  static constexpr int kStages = D == 128 ? 5 : 10;  // out, K and V tiles in flight
+  static constexpr int kOffQ = 0, kOffDo = kTile;
+  static constexpr int kOffRing = 2 * kTile;
+  static constexpr int kOffBar = kOffRing + kStages * kTile;
+  static constexpr int kOffXch = kOffBar + 512;  // [2][128] halves of D
+  static constexpr int kAlloc = kOffXch + 2 * kRows * 4;
 };
 
 struct RowBars {
-  uint64_t rows_full, rows_empty;  // Q, dout, out in shared memory
+  uint64_t rows_full, rows_empty;  // Q, dout in shared memory
+  uint64_t stats;                  // both halves of D exchanged, out read
   uint64_t ready;                  // Q and dout in TMEM
-  uint64_t kv_full[8], kv_empty[8];
+  uint64_t full[10], empty[10];
   uint64_t tail;
-  uint64_t s_full[2], ds_full[2];
+  uint64_t s_full, s_free, dp_full, ds_full;
   uint64_t dq_full, dq_empty;
   uint64_t drained;
   uint32_t tmem_base;
@@ -74,7 +77,7 @@ struct RowItem {
         tile(w.n_x - 1 - w.x),
         pos0(tile * P),
         n(window_len(p, b)),
-        kt(pos0, min(pos0 + P, n), p.window, p.sinks, kStepR) {
+        kt(pos0, min(pos0 + P, n), p.window, p.sinks, kRows) {
     steps = pos0 < n ? kt.n : 0;
   }
 };
@@ -87,11 +90,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = RowLayout<D>;
   constexpr int kStages = L::kStages;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr uint32_t kIdescS = tc::idesc_f16(kRows, kStepR, kBF16, false, false);
+  constexpr uint32_t kIdescS = tc::idesc_f16(kRows, kRows, kBF16, false, false);
   constexpr uint32_t kIdescQ = tc::idesc_f16(kRows, D, kBF16, false, true);
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   RowBars* bars = reinterpret_cast<RowBars*>(smem + L::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lg = __ffs(p.G) - 1, P = kRows >> lg;
@@ -99,16 +101,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->rows_full, 1);
     tc::mbar_init(&bars->rows_empty, kWorkers);
+    tc::mbar_init(&bars->stats, kWorkers);
     tc::mbar_init(&bars->ready, kWorkers);
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&bars->kv_full[s], 1);
-      tc::mbar_init(&bars->kv_empty[s], 1);
+      tc::mbar_init(&bars->full[s], 1);
+      tc::mbar_init(&bars->empty[s], 1);
     }
     tc::mbar_init(&bars->tail, 1);
-    for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&bars->s_full[s], 1);
-      tc::mbar_init(&bars->ds_full[s], kRows);
-    }
+    tc::mbar_init(&bars->s_full, 1);
+    tc::mbar_init(&bars->s_free, kWorkers);
+    tc::mbar_init(&bars->dp_full, 1);
+    tc::mbar_init(&bars->ds_full, kWorkers);
     tc::mbar_init(&bars->dq_full, 1);
     tc::mbar_init(&bars->dq_empty, kWorkers);
     tc::mbar_init(&bars->drained, 1);
@@ -134,50 +137,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   // grid's end before it reads lse2 and D
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
+  // ring tiles of an item: out, then K and V of each step
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     if (blockIdx.x == 0) begin_status(p, lane);
-    int kv = 0, items = 0, tails = 0;
+    int x = 0, items = 0, tails = 0;
     for (ItemWalk it(p.n_tiles, p.Hkv, p.B); ok && it.any(); it.next()) {
       const RowItem w(p, P, it);
       if (w.steps == 0) continue;
-      if (items > 0) ok = warp_wait(&bars->rows_empty, items - 1);
-      if (!ok) break;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(&bars->rows_full, 3 * L::kRowTile);
-        for (int kc = 0; kc < L::KC; ++kc) {
-          uint8_t* dst = smem + kc * L::kRowChunk;
-          tc::tma_load_4d(dst + L::kOffQ, &tm_q, &bars->rows_full, kc * 64, w.g * p.G, w.pos0, w.b);
-          tc::tma_load_4d(dst + L::kOffDo, &tm_do, &bars->rows_full, kc * 64, w.g * p.G, w.pos0, w.b);
-          tc::tma_load_4d(dst + L::kOffO, &tm_o, &bars->rows_full, kc * 64, w.g * p.G, w.pos0, w.b);
-        }
-      }
-      ++items;
-      for (int i = 0; ok && i < w.steps; ++i, ++kv) {
-        const int st = kv % kStages, tok0 = w.kt.tile(i) * kStepR;
-        if (kv >= kStages) ok = warp_wait(&bars->kv_empty[st], (kv / kStages) - 1);
+      for (int i = 0; ok && i <= 2 * w.steps; ++i, ++x) {
+        const int st = x % kStages;
+        if (x >= kStages) ok = warp_wait(&bars->empty[st], x / kStages - 1);
         if (!ok) break;
-        uint8_t* dst = smem + L::kOffKV + st * 2 * L::kKeyTile;
-        const bool clear = tok0 + kStepR > w.n && w.n < p.S;
-        uint64_t* bar = clear ? &bars->tail : &bars->kv_full[st];
+        uint8_t* dst = smem + L::kOffRing + st * L::kTile;
+        const int tok0 = i > 0 ? w.kt.tile((i - 1) >> 1) * kRows : 0;
+        const bool is_k = i & 1;
+        const bool clear = is_k && tok0 + kRows > w.n && w.n < p.S;
+        uint64_t* bar = clear ? &bars->tail : &bars->full[st];
         if (lane == 0) {
-          tc::mbar_arrive_expect_tx(bar, 2 * L::kKeyTile);
+          tc::mbar_arrive_expect_tx(bar, L::kTile);
           for (int kc = 0; kc < L::KC; ++kc) {
-            tc::tma_load_4d(dst + kc * L::kKeyChunk, &tm_k, bar, kc * 64, w.g, tok0, w.b);
-            tc::tma_load_4d(dst + L::kKeyTile + kc * L::kKeyChunk, &tm_v, bar, kc * 64, w.g, tok0, w.b);
+            if (i == 0)
+              tc::tma_load_4d(dst + kc * L::kChunk, &tm_o, bar, kc * 64, w.g * p.G, w.pos0, w.b);
+            else
+              tc::tma_load_4d(dst + kc * L::kChunk, is_k ? &tm_k : &tm_v, bar, kc * 64, w.g, tok0, w.b);
           }
         }
         if (clear) {
           // dS is 0 there, but 0 x NaN is not
           ok = warp_wait(&bars->tail, tails++);
-          zero_tile_rows(dst, L::KC, kStepR, w.n - tok0, lane);
-          if (lane == 0) tc::mbar_arrive(&bars->kv_full[st]);
+          zero_tile_rows(dst, L::KC, kRows, w.n - tok0, lane);
+          if (lane == 0) tc::mbar_arrive(&bars->full[st]);
+        }
+        if (i == 0) {
+          if (items > 0) ok = ok && warp_wait(&bars->rows_empty, items - 1);
+          if (!ok) {
+            ++x;
+            break;
+          }
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(&bars->rows_full, 2 * L::kTile);
+            for (int kc = 0; kc < L::KC; ++kc) {
+              tc::tma_load_4d(smem + L::kOffQ + kc * L::kChunk, &tm_q, &bars->rows_full, kc * 64, w.g * p.G, w.pos0,
+                              w.b);
+              tc::tma_load_4d(smem + L::kOffDo + kc * L::kChunk, &tm_do, &bars->rows_full, kc * 64, w.g * p.G, w.pos0,
+                              w.b);
+            }
+          }
+          ++items;
         }
       }
     }
     // every copy lands before the CTA retires
     if (items > 0) tc::mbar_wait(&bars->rows_full, (items - 1) & 1);
-    for (int j = max(0, kv - kStages); j < kv; ++j) tc::mbar_wait(&bars->kv_full[j % kStages], (j / kStages) & 1);
+    for (int j = max(0, x - kStages); j < x; ++j) tc::mbar_wait(&bars->full[j % kStages], (j / kStages) & 1);
     if (!ok) raise_status(p.status, kTimeout, 331);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -186,69 +199,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       return ok;
     };
-    const uint64_t k0 = tc::smem_desc_sw128(smem + L::kOffKV, 16, 1024);
-    const uint64_t v0 = tc::smem_desc_sw128(smem + L::kOffKV + L::kKeyTile, 16, 1024);
-    const uint64_t kmn0 = tc::smem_desc_sw128(smem + L::kOffKV, L::kKeyChunk, 1024);
-    int kv = 0, items = 0;
+    const uint64_t r0 = tc::smem_desc_sw128(smem + L::kOffRing, 16, 1024);
+    const uint64_t rmn0 = tc::smem_desc_sw128(smem + L::kOffRing, L::kChunk, 1024);
+    auto at = [&](int x) { return (uint64_t)(((x % kStages) * L::kTile) >> 4); };
+    // S or dP: A from TMEM, B = the ring tile x
+    auto issue = [&](uint32_t dst, uint32_t a, int x, uint64_t* bar) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc::mma_f16_ts_w(tmem + dst, tmem + a + k * 8,
+                         r0 + at(x) + (uint64_t)((((k >> 2) * L::kChunk) + (k & 3) * 32) >> 4), kIdescS,
+                         k > 0 ? 1u : 0u);
+      tc::mma_commit_w(bar);
+    };
+    int x = 0, items = 0, step = 0;  // x: the item's first ring tile (out)
     for (ItemWalk it(p.n_tiles, p.Hkv, p.B); ok && it.any(); it.next()) {
       const RowItem w(p, P, it);
       if (w.steps == 0) continue;
-      if (!wait(&bars->ready, items)) break;
-      // dQ += dS K of the item's step j (step x of the CTA)
-      auto issue_dq = [&](int j) {
-        const int x = kv + j;
-        if (j == 0 && items > 0 && !wait(&bars->dq_empty, items - 1)) return;
-        if (!wait(&bars->ds_full[x & 1], x >> 1)) return;
-        const uint64_t kd = kmn0 + (uint64_t)(((x % kStages) * 2 * L::kKeyTile) >> 4);
-#pragma unroll
-        for (int k = 0; k < kStepR / 16; ++k)
-          tc::mma_f16_ts_w(tmem + kColDQ, tmem + kColBuf + (x & 1) * 128 + k * 8, kd + (uint64_t)((k * 2048) >> 4),
-                           kIdescQ, (j > 0 || k > 0) ? 1u : 0u);
-        tc::mma_commit_w(&bars->kv_empty[x % kStages]);
+      auto s_of = [&](int i) {
+        const int k = x + 1 + 2 * i;
+        if (wait(&bars->full[k % kStages], k / kStages)) issue(kColSR, 0, k, &bars->s_full);
       };
+      auto dp_of = [&](int i) {
+        const int v = x + 2 + 2 * i;
+        if (!wait(&bars->full[v % kStages], v / kStages)) return;
+        issue(kColDPR, D / 2, v, &bars->dp_full);
+        tc::mma_commit_w(&bars->empty[v % kStages]);
+      };
+      if (!wait(&bars->ready, items)) break;
+      s_of(0);
+      if (ok) dp_of(0);
       for (int i = 0; ok && i < w.steps; ++i) {
-        const int x = kv + i;
-        if (!wait(&bars->kv_full[x % kStages], x / kStages)) break;
-        const uint64_t off = (uint64_t)(((x % kStages) * 2 * L::kKeyTile) >> 4);
-        const uint32_t s_tm = tmem + kColBuf + (x & 1) * 128;
+        const int k = x + 1 + 2 * i;
+        if (!wait(&bars->s_free, step + i)) break;
+        if (i + 1 < w.steps) s_of(i + 1);
+        if (i == 0 && items > 0) wait(&bars->dq_empty, items - 1);
+        if (!ok || !wait(&bars->ds_full, step + i)) break;
+        // dQ += dS K: keys 0-63 of the operand packed at dP's column 0, 64-127 at its column 64
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t o = off + (uint64_t)((((k >> 2) * L::kKeyChunk) + (k & 3) * 32) >> 4);
-          tc::mma_f16_ts_w(s_tm, tmem + k * 8, k0 + o, kIdescS, k > 0 ? 1u : 0u);
-        }
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t o = off + (uint64_t)((((k >> 2) * L::kKeyChunk) + (k & 3) * 32) >> 4);
-          tc::mma_f16_ts_w(s_tm + 64, tmem + D / 2 + k * 8, v0 + o, kIdescS, k > 0 ? 1u : 0u);
-        }
-        tc::mma_commit_w(&bars->s_full[x & 1]);
-        if (i > 0) issue_dq(i - 1);
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          tc::mma_f16_ts_w(tmem + kColDQ, tmem + kColDPR + (kk >> 2) * 64 + (kk & 3) * 8,
+                           rmn0 + at(k) + (uint64_t)((kk * 2048) >> 4), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
+        if (i == w.steps - 1) tc::mma_commit_w(&bars->dq_full);
+        tc::mma_commit_w(&bars->empty[k % kStages]);
+        if (i + 1 < w.steps) dp_of(i + 1);
       }
-      if (ok) issue_dq(w.steps - 1);
       if (!ok) break;
-      tc::mma_commit_w(&bars->dq_full);
-      kv += w.steps;
+      x += 1 + 2 * w.steps;
+      step += w.steps;
       ++items;
     }
     if (!ok) raise_status(p.status, kTimeout, 332);
     tc::mma_commit_w(&bars->drained);
     tc::mbar_wait(&bars->drained, 0);
   } else {
-    // ------------------------------------------------------------ rows
-    const int wg = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+    // ------------------------------------------------------------ workers
+    const int half = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
     const uint32_t tb = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t s_tm = tb + kColSR + half * 64, d_tm = tb + kColDPR + half * 64;
     const float sc = rsqrtf((float)D) * kLog2e;
+    float* xch = reinterpret_cast<float*>(smem + L::kOffXch) + r;
     float lse2 = 0.f, dd = 0.f;  // of the current item's row
-    int items = 0, step = 0;
+    int x = 0, items = 0, step = 0;
 
-    // the first item with steps from `it` on; tiles behind the sequence's end
-    // get dq = 0 and lse2 = inf (p = 0) on the way
+    // on to the first item with steps; tiles behind the sequence's end get
+    // dq = 0 and lse2 = inf (p = 0) on the way
     auto seek = [&](ItemWalk& it) {
       for (; it.any(); it.next()) {
         const RowItem w(p, P, it);
         if (w.steps > 0) break;
         const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
-        if (wg == 0) {
+        if (half == 0) {
           const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
           p.lse2[at] = -kNegInf;
           p.dd[at] = 0.f;
@@ -256,120 +276,175 @@ __global__ void __launch_bounds__(kThreads, 1)
           T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb + (int64_t)pos * p.dq.ss +
                    (int64_t)head * p.dq.sh;
 #pragma unroll
-          for (int x = 0; x < D / 8; ++x) *reinterpret_cast<uint4*>(dst + x * 8) = make_uint4(0u, 0u, 0u, 0u);
+          for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(dst + e * 8) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
     };
-    // Q (warps 0-3) and dout (4-7) into TMEM, D = dout . out and lse2
-    auto load_rows = [&](const ItemWalk& it) {
+    // lse2 and D = dout . out of an item's row: each half takes half of the
+    // columns
+    auto row_stats = [&](const ItemWalk& it) {
       const RowItem w(p, P, it);
       const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
       const bool live = pos < w.n;
       lse2 = live ? p.lse[((int64_t)w.b * p.H + head) * p.S + pos] * kLog2e : -kNegInf;
-      if (!warp_wait(&bars->rows_full, items)) return false;
+      ok = warp_wait(&bars->rows_full, items) && ok;
+      ok = warp_wait(&bars->full[x % kStages], x / kStages) && ok;
+      const uint8_t* po = smem + L::kOffRing + (x % kStages) * L::kTile + r * 128;
+      const uint8_t* pd = smem + L::kOffDo + r * 128;
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int cc = 0; cc < L::KC; ++cc) {
-        const uint8_t* base = smem + cc * L::kRowChunk + r * 128;
-        uint32_t w32[32];
+      for (int v = 0; v < D / 16; ++v) {
+        const int e = half * (D / 16) + v;  // 16-byte piece of the row
+        const int at = (e >> 3) * L::kChunk + (((e & 7) ^ (r & 7)) << 4);
+        float fd[8], fo[8];
+        Elt<T>::to_float(*reinterpret_cast<const uint4*>(pd + at), fd);
+        Elt<T>::to_float(*reinterpret_cast<const uint4*>(po + at), fo);
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const int at = (v ^ (r & 7)) * 16;
-          const uint4 xd = *reinterpret_cast<const uint4*>(base + L::kOffDo + at);
-          const uint4 xo = *reinterpret_cast<const uint4*>(base + L::kOffO + at);
-          const uint4 xt = wg == 0 ? *reinterpret_cast<const uint4*>(base + L::kOffQ + at) : xd;
-          w32[4 * v] = xt.x, w32[4 * v + 1] = xt.y, w32[4 * v + 2] = xt.z, w32[4 * v + 3] = xt.w;
-          float fd[8], fo[8];
-          Elt<T>::to_float(xd, fd);
-          Elt<T>::to_float(xo, fo);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e & 3] = fmaf(fd[e], fo[e], acc[e & 3]);
-        }
-        tc::tmem_st32(tb + (wg == 0 ? 0 : D / 2) + cc * 32, w32);
+        for (int e2 = 0; e2 < 8; ++e2) acc[e2 & 3] = fmaf(fd[e2], fo[e2], acc[e2 & 3]);
       }
-      dd = live ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : 0.f;
-      if (wg == 0) {
+      const float mine = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      xch[half * kRows] = mine;
+      tc::mbar_arrive(&bars->stats);
+      ok = warp_wait(&bars->stats, items) && ok;
+      const float a = half == 0 ? mine : xch[0], b = half == 0 ? xch[kRows] : mine;
+      dd = live ? a + b : 0.f;  // the same sum in both halves
+      if (threadIdx.x == 0) tc::mbar_arrive(&bars->empty[x % kStages]);  // every worker has read out
+      if (half == 0) {
         const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
         p.lse2[at] = lse2;
         p.dd[at] = dd;
+      }
+    };
+    // Q (half 0) and dout (half 1) into TMEM
+    auto rows_to_tmem = [&] {
+      const uint8_t* src = smem + (half == 0 ? L::kOffQ : L::kOffDo) + r * 128;
+#pragma unroll
+      for (int cc = 0; cc < L::KC; ++cc) {
+        uint32_t w32[32];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const uint4 t = *reinterpret_cast<const uint4*>(src + cc * L::kChunk + ((v ^ (r & 7)) << 4));
+          w32[4 * v] = t.x, w32[4 * v + 1] = t.y, w32[4 * v + 2] = t.z, w32[4 * v + 3] = t.w;
+        }
+        tc::tmem_st32(tb + half * (D / 2) + cc * 32, w32);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(&bars->rows_empty);
       tc::mbar_arrive(&bars->ready);
-      return true;
     };
 
     ItemWalk it(p.n_tiles, p.Hkv, p.B);
     seek(it);
-    if (it.any()) ok = load_rows(it);
+    if (it.any()) {
+      row_stats(it);
+      if (ok) rows_to_tmem();
+    }
     while (ok && it.any()) {
       const RowItem w(p, P, it);
-      const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
+      const int pos = w.pos0 + (r >> lg);
       const int lo = pos - p.window + 1;
-      const int lo_b = w.pos0 + P - p.window;  // the last row's lo
-      for (int i = (step & 1) == wg ? 0 : 1; i < w.steps; i += 2) {
-        const int x = step + i, tok0 = w.kt.tile(i) * kStepR;
-        const uint32_t s_tm = tb + kColBuf + (x & 1) * 128;
-        if (!(ok = warp_wait(&bars->s_full[x & 1], x >> 1))) break;
+      // the warp's rows: first and last position
+      const int pos_a = w.pos0 + ((q4 * 32) >> lg), pos_b = w.pos0 + ((q4 * 32 + 31) >> lg);
+      for (int i = 0; i < w.steps; ++i) {
+        const int y = step + i, key0 = w.kt.tile(i) * kRows + half * 64;  // the warp's keys [key0, key0 + 64)
+        // none of the warp's pairs is visible, or all are
+        const bool none = key0 > pos_b || (key0 + 63 < pos_a - p.window + 1 && key0 >= p.sinks);
+        const bool all = key0 + 63 <= pos_a && key0 >= pos_b - p.window + 1;
+        if (!(ok = warp_wait(&bars->s_full, y))) break;
         tc::fence_after_sync();
-        const bool edge = tok0 + kStepR - 1 > w.pos0 || tok0 < lo_b;
-        const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-lse2, -lse2), nd2 = make_float2(-dd, -dd);
+        uint32_t pf[64];
+        tc::tmem_ld32(s_tm, pf);
+        tc::tmem_ld32(s_tm + 32, pf + 32);
+        tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&bars->s_free);
+        if (!none) {
+          const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-lse2, -lse2);
+          auto scaled = [&](int j) {
+            return __ffma2_rn(make_float2(__uint_as_float(pf[2 * j]), __uint_as_float(pf[2 * j + 1])), sc2, off2);
+          };
+          float2 a = scaled(0), b = scaled(1);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float2 c = a, e = b;
+            pf[2 * j] = __float_as_uint(ex2_placed(a.x));
+            if (j + 2 < 32) c = scaled(j + 2);
+            pf[2 * j + 1] = __float_as_uint(ex2_placed(a.y));
+            pf[2 * j + 2] = __float_as_uint(ex2_placed(b.x));
+            if (j + 2 < 32) e = scaled(j + 3);
+            pf[2 * j + 3] = __float_as_uint(ex2_placed(b.y));
+            a = c;
+            b = e;
+          }
+        }
+        if (!(ok = warp_wait(&bars->dp_full, y))) break;
+        tc::fence_after_sync();
+        uint32_t m[2] = {0xffffffffu, 0xffffffffu};
+        if (!all) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int t0 = key0 + c * 32;
+            m[c] = none ? 0u : bit_range(lo - t0, pos - t0) | bit_range(0, min(pos, p.sinks - 1) - t0);
+          }
+        }
+        const float2 nd2 = make_float2(-dd, -dd);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t sv[32], pv[32], dw[16];
-          tc::tmem_ld32(s_tm + c * 32, sv);
-          tc::tmem_ld32(s_tm + 64 + c * 32, pv);
+          uint32_t dv[32], dw[16];
+          tc::tmem_ld32(d_tm + c * 32, dv);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), sc2, off2);
-            const float2 e = make_float2(tc::ex2(y.x), tc::ex2(y.y));
-            const float2 d =
-                __fadd2_rn(make_float2(__uint_as_float(pv[j]), __uint_as_float(pv[j + 1])), nd2);
-            const float2 ds = __fmul2_rn(e, d);
-            sv[j] = __float_as_uint(ds.x);
-            sv[j + 1] = __float_as_uint(ds.y);
+            const int e = c * 32 + j;
+            const float2 ds = __fmul2_rn(make_float2(__uint_as_float(pf[e]), __uint_as_float(pf[e + 1])),
+                                         __fadd2_rn(make_float2(__uint_as_float(dv[j]), __uint_as_float(dv[j + 1])),
+                                                    nd2));
+            dw[j >> 1] = pack2<T>(ds.x, ds.y);
           }
-          if (edge) {
-            const int t0 = tok0 + c * 32;
-            const uint32_t seen = bit_range(lo - t0, pos - t0) | bit_range(0, min(pos, p.sinks - 1) - t0);
+          if (!all) {
+            // hidden pairs are cleared after the products: what they hold may not be finite
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(seen & (1u << j))) sv[j] = 0u;
+            for (int j = 0; j < 16; ++j)
+              dw[j] &= (m[c] >> (2 * j) & 1u ? 0xffffu : 0u) | (m[c] >> (2 * j + 1) & 1u ? 0xffff0000u : 0u);
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) dw[j] = pack2<T>(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
-          tc::tmem_st16(s_tm + c * 16, dw);
+          tc::tmem_st16(d_tm + c * 16, dw);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->ds_full[x & 1]);
+        tc::mbar_arrive(&bars->ds_full);
       }
       step += w.steps;
-      if (!ok || !(ok = warp_wait(&bars->dq_full, items))) break;
-      tc::fence_after_sync();
-      ++items;
+      x += 1 + 2 * w.steps;
+      const int item = items++;
       it.next();
       seek(it);
-      if (it.any() && !(ok = load_rows(it))) break;
-      // ---- dq of this item, each group half of the columns
-      T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb +
-               (int64_t)min(pos, p.S - 1) * p.dq.ss + (int64_t)head * p.dq.sh;
-      const bool live = pos < w.n;
+      const bool more = it.any();
+      if (more) row_stats(it);  // (while the last dQ runs)
+      if (!ok || !(ok = warp_wait(&bars->dq_full, item))) break;
+      tc::fence_after_sync();
+      if (more) rows_to_tmem();
+      // ---- dq of the item, 64 columns a warp (half 0 all of them at D = 64)
+      if (half < L::KC) {
+        const bool live = pos < w.n;
+        uint4 row[8];
 #pragma unroll
-      for (int cc = wg * (D / 64); cc < (wg + 1) * (D / 64); ++cc) {
-        uint32_t v[32];
-        tc::tmem_ld32(tb + kColDQ + cc * 32, v);
-        tc::tmem_wait_ld();
-        if (!live) {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tc::tmem_ld32(tb + kColDQ + half * 64 + c * 32, v);
+          tc::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0u;
+          for (int e = 0; e < 4; ++e)
+            row[c * 4 + e] = live ? pack8<T>(v + e * 8, rsqrtf((float)D)) : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (pos < p.S) {
+        transpose8(row, lane);
+        T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb + half * 64 + (lane & 7) * 8;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4*>(dst + cc * 32 + x * 8) = pack8<T>(v + x * 8, rsqrtf((float)D));
+        for (int e = 0; e < 8; ++e) {
+          const int rr = q4 * 32 + (lane & 24) + e, pp = w.pos0 + (rr >> lg);
+          if (pp < p.S)
+            *reinterpret_cast<uint4*>(dst + (int64_t)pp * p.dq.ss +
+                                      (int64_t)(w.g * p.G + (rr & (p.G - 1))) * p.dq.sh) = row[e];
         }
       }
       tc::fence_before_sync();
@@ -423,7 +498,7 @@ struct KeyBars {
   uint64_t kv_full, kv_empty;
   uint64_t q_full[kNS], q_empty[kNS];
   uint64_t tail;
-  uint64_t s_full, dp_full, p_full, ds_full;
+  uint64_t s_full, dp_full, p_full[2], ds_full;
   uint64_t acc_full, acc_empty;
   uint64_t drained;
   uint32_t tmem_base;
@@ -464,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   KeyBars* bars = reinterpret_cast<KeyBars*>(smem + L::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lgp = 8 - __ffs(p.G), P = 1 << lgp;  // positions of a row tile
+  const int lg = __ffs(p.G) - 1, lgp = 7 - lg, P = 1 << lgp;  // positions of a row tile
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->kv_full, 1);
@@ -476,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&bars->tail, 1);
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->p_full, kWorkers);
+    for (int c = 0; c < 2; ++c) tc::mbar_init(&bars->p_full[c], kWorkers);
     tc::mbar_init(&bars->ds_full, kWorkers);
     tc::mbar_init(&bars->acc_full, 1);
     tc::mbar_init(&bars->acc_empty, kWorkers);
@@ -571,13 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::mma_commit_w(bar);
     };
-    // dV or dK: contraction over the tile's rows; rows 0-63 of the operand are
-    // packed at col, rows 64-127 at col + 64 (each worker half's own columns)
-    auto issue_ts = [&](uint32_t dst, uint32_t col, uint64_t b, bool first) {
-#pragma unroll
-      for (int k = 0; k < kRows / 16; ++k)
-        tc::mma_f16_ts_w(tmem + dst, tmem + col + (k >> 2) * 64 + (k & 3) * 8, b + (uint64_t)((k * 2048) >> 4),
-                         kIdescKV, (!first || k > 0) ? 1u : 0u);
+    // dV or dK: contraction over the tile's rows, slices of 16; rows 0-63 of
+    // the operand are packed at col, rows 64-127 at col + 64 (each worker
+    // half's own columns)
+    auto issue_ts = [&](uint32_t dst, uint32_t col, uint64_t b, int k, bool first) {
+      tc::mma_f16_ts_w(tmem + dst, tmem + col + (k >> 2) * 64 + (k & 3) * 8, b + (uint64_t)((k * 2048) >> 4),
+                       kIdescKV, first ? 0u : 1u);
     };
     const uint64_t tile16 = (uint64_t)(L::kTile >> 4);
     int q = 0, items = 0;
@@ -591,14 +665,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n; ++i) {
         const int x = q + i;
         if (i == 0 && items > 0 && !wait(&bars->acc_empty, items - 1)) break;
-        if (!wait(&bars->p_full, x)) break;
-        issue_ts(kColDV, kColST, qmn0 + tile16 + stage(x), i == 0);
+        // the rows of the workers' first 32 columns, then those of the second
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (!wait(&bars->p_full[c], x)) break;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            issue_ts(kColDV, kColST, qmn0 + tile16 + stage(x), (k >> 1) * 4 + c * 2 + (k & 1),
+                     i == 0 && c == 0 && k == 0);
+        }
+        if (!ok) break;
         if (i + 1 < n) {
           if (!wait(&bars->q_full[(x + 1) % kNS], (x + 1) / kNS)) break;
           issue_ss(kColST, kd, q0 + stage(x + 1), &bars->s_full);
         }
         if (!wait(&bars->ds_full, x)) break;
-        issue_ts(kColDK, kColDPT, qmn0 + stage(x), i == 0);
+#pragma unroll
+        for (int k = 0; k < kRows / 16; ++k)
+          issue_ts(kColDK, kColDPT, qmn0 + stage(x), k, i == 0 && k == 0);
         tc::mma_commit_w(&bars->q_empty[x % kNS]);
         if (i + 1 < n) issue_ss(kColDPT, vd, q0 + tile16 + stage(x + 1), &bars->dp_full);
       }
@@ -624,7 +708,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = w.t0; t < w.t1; ++t, ++q) {
         const int st = q % kNS, pos0 = t * P;
         const float* info = reinterpret_cast<const float*>(smem + L::kOffInfo + st * 1024) + half * 64;
-        const bool edge = pos0 < w.k0 + kRows - 1 || pos0 + P - 1 > w.k0 + p.window - 1;
+        // the warp's keys [key_a, key_a + 32) and rows, from position pos_a to
+        // pos_b: none of their pairs is visible, or all are
+        const int key_a = w.k0 + q4 * 32, pos_a = pos0 + ((half * 64) >> lg), pos_b = pos0 + ((half * 64 + 63) >> lg);
+        const bool none = pos_b < key_a || (pos_a > key_a + 31 + p.window - 1 && key_a >= p.sinks);
+        const bool all = pos_a >= key_a + 31 && pos_b <= key_a + p.window - 1;
         // ---- P^T
         if (!(ok = warp_wait(&bars->q_full[st], q / kNS) && warp_wait(&bars->s_full, q))) break;
         tc::fence_after_sync();
@@ -633,41 +721,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld32(s_tm, pf);
         tc::tmem_ld32(s_tm + 32, pf + 32);
         tc::tmem_wait_ld();
-        const float2 sc2 = make_float2(sc, sc);
-#pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(info + j);
-          const float2 a = __ffma2_rn(make_float2(__uint_as_float(pf[j]), __uint_as_float(pf[j + 1])), sc2,
-                                      make_float2(-l4.x, -l4.y));
-          const float2 b = __ffma2_rn(make_float2(__uint_as_float(pf[j + 2]), __uint_as_float(pf[j + 3])), sc2,
-                                      make_float2(-l4.z, -l4.w));
-          pf[j] = __float_as_uint(tc::ex2(a.x));
-          pf[j + 1] = __float_as_uint(tc::ex2(a.y));
-          pf[j + 2] = __float_as_uint(tc::ex2(b.x));
-          pf[j + 3] = __float_as_uint(tc::ex2(b.y));
-        }
-        if (edge) {
-          // rows from the key's own on, to the last whose window holds it
-          const int64_t ca = (int64_t)(key - pos0) * p.G;
-          const int64_t cb = key < p.sinks ? kRows : ((int64_t)key + p.window - pos0) * p.G;
+        uint32_t m[2] = {0xffffffffu, 0xffffffffu};  // visible rows
+        if (!all) {
+          // from the key's own row on, to the last whose window holds it
+          const int64_t ca = (int64_t)(key - pos0) << lg;
+          const int64_t cb = key < p.sinks ? kRows : ((int64_t)key + p.window - pos0) << lg;
           const int a = (int)max((int64_t)-1, min((int64_t)kRows, ca)) - half * 64;
           const int b = (int)max((int64_t)0, min((int64_t)kRows, cb)) - 1 - half * 64;
-          const uint32_t m0 = bit_range(a, b), m1 = bit_range(a - 32, b - 32);
+          m[0] = none ? 0u : bit_range(a, b);
+          m[1] = none ? 0u : bit_range(a - 32, b - 32);
+        }
+        const float2 sc2 = make_float2(sc, sc);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (!(m0 & (1u << j))) pf[j] = 0u;
-            if (!(m1 & (1u << j))) pf[32 + j] = 0u;
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pw[16];
+          if (none) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) pf[c * 32 + j] = 0u;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pw[j] = 0u;
+          } else {
+            auto scaled = [&](int j, float2* y) {  // logits of rows j .. j + 3 minus their log-sum-exps
+              const float4 l4 = *reinterpret_cast<const float4*>(info + c * 32 + j);
+              const uint32_t* v = pf + c * 32 + j;
+              y[0] = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), sc2,
+                                make_float2(-l4.x, -l4.y));
+              y[1] = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), sc2,
+                                make_float2(-l4.z, -l4.w));
+            };
+            float2 y[2], next[2];
+            scaled(0, y);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              uint32_t* v = pf + c * 32 + j;
+              v[0] = __float_as_uint(ex2_placed(y[0].x));
+              v[1] = __float_as_uint(ex2_placed(y[0].y));
+              if (j + 4 < 32) scaled(j + 4, next);
+              v[2] = __float_as_uint(ex2_placed(y[1].x));
+              v[3] = __float_as_uint(ex2_placed(y[1].y));
+              if (!all) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (!(m[c] & (1u << (j + u)))) v[u] = 0u;
+              }
+              y[0] = next[0];
+              y[1] = next[1];
+              pw[j / 2] = pack2<T>(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              pw[j / 2 + 1] = pack2<T>(__uint_as_float(v[2]), __uint_as_float(v[3]));
+            }
           }
+          tc::tmem_st16(s_tm + c * 16, pw);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          tc::mbar_arrive(&bars->p_full[c]);
         }
-        {
-          uint32_t pw[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) pw[j] = pack2<T>(__uint_as_float(pf[2 * j]), __uint_as_float(pf[2 * j + 1]));
-          tc::tmem_st32(s_tm, pw);
-        }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        tc::mbar_arrive(&bars->p_full);
         // ---- dS^T
         if (!(ok = warp_wait(&bars->dp_full, q))) break;
         tc::fence_after_sync();
@@ -707,36 +814,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float ksc = rsqrtf((float)D);
       const bool live = key < w.n;
+      // 64 columns of dk and of dv a warp (D = 64: dk in half 0, dv in half 1)
 #pragma unroll 1
-      for (int cc = half * (D / 64); cc < (half + 1) * (D / 64); ++cc) {
-        uint32_t v[32], d[32];
+      for (int o = 0; o < 2; ++o) {
+        const bool is_v = D == 64 ? half : o;
+        if (D == 64 && o > 0) break;
+        const int col = D == 64 ? 0 : half * 64;
+        uint32_t v[64];
         if (any) {
-          tc::tmem_ld32(tb + kColDV + cc * 32, v);
-          tc::tmem_ld32(tb + kColDK + cc * 32, d);
+          const uint32_t src = tb + (is_v ? kColDV : kColDK) + col;
+          tc::tmem_ld32(src, v);
+          tc::tmem_ld32(src + 32, v + 32);
           tc::tmem_wait_ld();
         }
         if (!any || !live) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = d[j] = 0u;
+          for (int j = 0; j < 64; ++j) v[j] = 0u;
         }
         if (w.slot >= 0) {
           // [b, g][slot][dk, dv][128][D] fp32
-          float* dst = p.part + ((((int64_t)(w.b * p.Hkv + w.g) * (p.n_chunks + 1) + w.slot) * 2) * kRows + k) * D +
-                       cc * 32;
+          float* dst = p.part + ((((int64_t)(w.b * p.Hkv + w.g) * (p.n_chunks + 1) + w.slot) * 2 + is_v) * kRows + k) * D +
+                       col;
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            *reinterpret_cast<uint4*>(dst + x) = make_uint4(d[x], d[x + 1], d[x + 2], d[x + 3]);
-            *reinterpret_cast<uint4*>(dst + kRows * D + x) = make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
-          }
-        } else if (key < p.S) {
-          T* dk = static_cast<T*>(const_cast<void*>(p.dk.data)) + (int64_t)w.b * p.dk.sb + (int64_t)key * p.dk.ss +
-                  (int64_t)w.g * p.dk.sh + cc * 32;
-          T* dv = static_cast<T*>(const_cast<void*>(p.dv.data)) + (int64_t)w.b * p.dv.sb + (int64_t)key * p.dv.ss +
-                  (int64_t)w.g * p.dv.sh + cc * 32;
+          for (int e = 0; e < 64; e += 4)
+            *reinterpret_cast<uint4*>(dst + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else {
+          uint4 row[8];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            *reinterpret_cast<uint4*>(dk + x * 8) = pack8<T>(d + x * 8, ksc);
-            *reinterpret_cast<uint4*>(dv + x * 8) = pack8<T>(v + x * 8, 1.f);
+          for (int e = 0; e < 8; ++e) row[e] = pack8<T>(v + e * 8, is_v ? 1.f : ksc);
+          transpose8(row, lane);
+          const View& out = is_v ? p.dv : p.dk;
+          T* dst = static_cast<T*>(const_cast<void*>(out.data)) + (int64_t)w.b * out.sb + (int64_t)w.g * out.sh + col +
+                   (lane & 7) * 8;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int kk = w.k0 + q4 * 32 + (lane & 24) + e;
+            if (kk < p.S) *reinterpret_cast<uint4*>(dst + (int64_t)kk * out.ss) = row[e];
           }
         }
       }
@@ -808,13 +921,12 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
   CUtensorMap mq, mdo, mo, mk, mv;
   if (!make_map(&mq, p.q, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
       !make_map(&mdo, p.dout, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
-      !make_map(&mo, p.out, p.dtype, p.B, p.S, p.H, D, p.G, P))
+      !make_map(&mo, p.out, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
+      !make_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows) ||
+      !make_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows))
     return cudaErrorInvalidValue;
   {
     using L = RowLayout<D>;
-    if (!make_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kStepR) ||
-        !make_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kStepR))
-      return cudaErrorInvalidValue;
     auto kern = window_bwd_row_tc_kernel<T, D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
@@ -823,9 +935,6 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
   }
   {
     using L = KeyLayout<D>;
-    if (!make_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows) ||
-        !make_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows))
-      return cudaErrorInvalidValue;
     auto kern = window_bwd_key_tc_kernel<T, D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
