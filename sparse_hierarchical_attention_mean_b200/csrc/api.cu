@@ -1378,7 +1378,7 @@ void window_extent(int64_t s, int64_t* window, int64_t* sinks) {
 }
 
 struct WindowLayout {
-  size_t status, dd, lse2, part, total;
+  size_t status, dd, nlse2, part, total;
   int64_t n_tiles, n_chunks, chunk_tiles;
 };
 WindowLayout window_layout(const dash_tensor_t* q, const dash_tensor_t* k, int64_t window, int64_t sinks, bool bwd) {
@@ -1395,8 +1395,8 @@ WindowLayout window_layout(const dash_tensor_t* q, const dash_tensor_t* k, int64
   const int64_t pos = 128 / (q->h / k->h);  // positions of a row tile
   L.n_tiles = (q->s + pos - 1) / pos;
   const size_t rows = (size_t)q->b * k->h * L.n_tiles * 128 * 4;
-  L.lse2 = align256(L.dd + rows);
-  L.part = align256(L.lse2 + rows);
+  L.nlse2 = align256(L.dd + rows);
+  L.part = align256(L.nlse2 + rows);
   L.total = L.part;
   if (sinks > 0) {
     // row tiles past the band of the first 128 keys: chunks of an ordinary
@@ -1483,7 +1483,8 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
   p.dk = solid_view(dk);
   p.dv = solid_view(dv);
   p.dd = at<float>(workspace, L.dd);
-  p.lse2 = at<float>(workspace, L.lse2);
+  p.ndd = p.dd;
+  p.nlse2 = at<float>(workspace, L.nlse2);
   p.part = at<float>(workspace, L.part);
   p.n_tiles = (int)L.n_tiles;
   p.n_chunks = (int)L.n_chunks;

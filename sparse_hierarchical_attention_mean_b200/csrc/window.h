@@ -22,10 +22,11 @@ struct WindowParams {
   int window, sinks;
   const int32_t* seqlens;   // [B] or null: rows and keys from seqlens[b] on are not there
   float* lse;               // [B, H, S] natural log-sum-exp of the row's logits, or null
-  float* dd;                // dout . out: [B, H, S] (backward, CUDA-core path)
+  float* dd;                // [B, H, S] dout . out (backward, CUDA-core path)
   // backward, tensor-core path, in the order of the row tiles (128 / G
   // positions x G heads): [B, Hkv, n_tiles, 128]
-  float* lse2;              // lse in log2 units; inf on rows that are not there
+  float* nlse2;             // -lse in log2 units; -inf on rows that are not there
+  float* ndd;               // -dout . out
   int n_tiles;
   float* part;              // partial dk, dv of the first 128 keys [B, Hkv, n_chunks + 1, 2, 128, D]
   int n_chunks;             // items of chunk_tiles row tiles that see only sinks of the first 128 keys

@@ -100,20 +100,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->rows_full, 1);
-    tc::mbar_init(&bars->rows_empty, kWorkers);
-    tc::mbar_init(&bars->stats, kWorkers);
-    tc::mbar_init(&bars->ready, kWorkers);
+    tc::mbar_init(&bars->rows_empty, kWorkers / 32);
+    tc::mbar_init(&bars->stats, kWorkers / 32);
+    tc::mbar_init(&bars->ready, kWorkers / 32);
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&bars->full[s], 1);
       tc::mbar_init(&bars->empty[s], 1);
     }
     tc::mbar_init(&bars->tail, 1);
     tc::mbar_init(&bars->s_full, 1);
-    tc::mbar_init(&bars->s_free, kWorkers);
+    tc::mbar_init(&bars->s_free, kWorkers / 32);
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->ds_full, kWorkers);
+    tc::mbar_init(&bars->ds_full, kWorkers / 32);
     tc::mbar_init(&bars->dq_full, 1);
-    tc::mbar_init(&bars->dq_empty, kWorkers);
+    tc::mbar_init(&bars->dq_empty, kWorkers / 32);
     tc::mbar_init(&bars->drained, 1);
     tc::fence_barrier_init();
   }
@@ -142,9 +142,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     if (blockIdx.x == 0) begin_status(p, lane);
     int x = 0, items = 0, tails = 0;
-    for (ItemWalk it(p.n_tiles, p.Hkv, p.B); ok && it.any(); it.next()) {
+    ItemWalk it(p.n_tiles, p.Hkv, p.B);
+    auto seek = [&] {  // the first item with steps
+      while (it.any() && RowItem(p, P, it).steps == 0) it.next();
+    };
+    auto load_rows = [&] {  // Q and dout of an item, when the one before has left their place
+      if (items > 0) ok = ok && warp_wait(&bars->rows_empty, items - 1);
+      if (!ok) return;
       const RowItem w(p, P, it);
-      if (w.steps == 0) continue;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&bars->rows_full, 2 * L::kTile);
+        for (int kc = 0; kc < L::KC; ++kc) {
+          uint8_t* dst = smem + kc * L::kChunk;
+          tc::tma_load_4d(dst + L::kOffQ, &tm_q, &bars->rows_full, kc * 64, w.g * p.G, w.pos0, w.b);
+          tc::tma_load_4d(dst + L::kOffDo, &tm_do, &bars->rows_full, kc * 64, w.g * p.G, w.pos0, w.b);
+        }
+      }
+      ++items;
+    };
+    seek();
+    if (it.any()) load_rows();
+    while (ok && it.any()) {
+      const RowItem w(p, P, it);
+      it.next();
+      seek();
       for (int i = 0; ok && i <= 2 * w.steps; ++i, ++x) {
         const int st = x % kStages;
         if (x >= kStages) ok = warp_wait(&bars->empty[st], x / kStages - 1);
@@ -169,23 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           zero_tile_rows(dst, L::KC, kRows, w.n - tok0, lane);
           if (lane == 0) tc::mbar_arrive(&bars->full[st]);
         }
-        if (i == 0) {
-          if (items > 0) ok = ok && warp_wait(&bars->rows_empty, items - 1);
-          if (!ok) {
-            ++x;
-            break;
-          }
-          if (lane == 0) {
-            tc::mbar_arrive_expect_tx(&bars->rows_full, 2 * L::kTile);
-            for (int kc = 0; kc < L::KC; ++kc) {
-              tc::tma_load_4d(smem + L::kOffQ + kc * L::kChunk, &tm_q, &bars->rows_full, kc * 64, w.g * p.G, w.pos0,
-                              w.b);
-              tc::tma_load_4d(smem + L::kOffDo + kc * L::kChunk, &tm_do, &bars->rows_full, kc * 64, w.g * p.G, w.pos0,
-                              w.b);
-            }
-          }
-          ++items;
-        }
+        // the next item's rows, once this one's ring is filled
+        if (i == min(4, 2 * w.steps) && it.any()) load_rows();
       }
     }
     // every copy lands before the CTA retires
@@ -258,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tm = tb + kColSR + half * 64, d_tm = tb + kColDPR + half * 64;
     const float sc = rsqrtf((float)D) * kLog2e;
     float* xch = reinterpret_cast<float*>(smem + L::kOffXch) + r;
-    float lse2 = 0.f, dd = 0.f;  // of the current item's row
+    float nlse2 = 0.f, ndd = 0.f;  // -lse2 and -D of the current item's row
+    float lse_next = 0.f;          // the next item's log-sum-exp
     int x = 0, items = 0, step = 0;
 
     // on to the first item with steps; tiles behind the sequence's end get
@@ -270,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
         if (half == 0) {
           const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
-          p.lse2[at] = -kNegInf;
-          p.dd[at] = 0.f;
+          p.nlse2[at] = kNegInf;
+          p.ndd[at] = 0.f;
         } else if (pos < p.S) {
           T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb + (int64_t)pos * p.dq.ss +
                    (int64_t)head * p.dq.sh;
@@ -280,13 +287,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
+    // the log-sum-exp of an item's row, asked for one item ahead
+    auto ask_lse = [&](const ItemWalk& it) {
+      const RowItem w(p, P, it);
+      const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
+      if (pos < w.n) lse_next = p.lse[((int64_t)w.b * p.H + head) * p.S + pos];
+    };
     // lse2 and D = dout . out of an item's row: each half takes half of the
     // columns
     auto row_stats = [&](const ItemWalk& it) {
       const RowItem w(p, P, it);
-      const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
-      const bool live = pos < w.n;
-      lse2 = live ? p.lse[((int64_t)w.b * p.H + head) * p.S + pos] * kLog2e : -kNegInf;
+      const bool live = w.pos0 + (r >> lg) < w.n;
+      nlse2 = live ? -lse_next * kLog2e : kNegInf;
       ok = warp_wait(&bars->rows_full, items) && ok;
       ok = warp_wait(&bars->full[x % kStages], x / kStages) && ok;
       const uint8_t* po = smem + L::kOffRing + (x % kStages) * L::kTile + r * 128;
@@ -304,15 +316,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float mine = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       xch[half * kRows] = mine;
-      tc::mbar_arrive(&bars->stats);
+      warp_arrive(&bars->stats, lane);
       ok = warp_wait(&bars->stats, items) && ok;
       const float a = half == 0 ? mine : xch[0], b = half == 0 ? xch[kRows] : mine;
-      dd = live ? a + b : 0.f;  // the same sum in both halves
+      ndd = live ? -(a + b) : 0.f;  // the same sum in both halves
       if (threadIdx.x == 0) tc::mbar_arrive(&bars->empty[x % kStages]);  // every worker has read out
       if (half == 0) {
         const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
-        p.lse2[at] = lse2;
-        p.dd[at] = dd;
+        p.nlse2[at] = nlse2;
+        p.ndd[at] = ndd;
       }
     };
     // Q (half 0) and dout (half 1) into TMEM
@@ -330,18 +342,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      tc::mbar_arrive(&bars->rows_empty);
-      tc::mbar_arrive(&bars->ready);
+      warp_arrive(&bars->rows_empty, lane);
+      warp_arrive(&bars->ready, lane);
     };
 
     ItemWalk it(p.n_tiles, p.Hkv, p.B);
     seek(it);
     if (it.any()) {
+      ask_lse(it);
       row_stats(it);
       if (ok) rows_to_tmem();
     }
-    while (ok && it.any()) {
+    for (bool more = it.any(); ok && more;) {
       const RowItem w(p, P, it);
+      it.next();
+      seek(it);
+      more = it.any();
+      if (more) ask_lse(it);
       const int pos = w.pos0 + (r >> lg);
       const int lo = pos - p.window + 1;
       // the warp's rows: first and last position
@@ -358,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld32(s_tm + 32, pf + 32);
         tc::tmem_wait_ld();
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->s_free);
+        warp_arrive(&bars->s_free, lane);
         if (!none) {
-          const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-lse2, -lse2);
+          const float2 sc2 = make_float2(sc, sc), off2 = make_float2(nlse2, nlse2);
           auto scaled = [&](int j) {
             return __ffma2_rn(make_float2(__uint_as_float(pf[2 * j]), __uint_as_float(pf[2 * j + 1])), sc2, off2);
           };
@@ -380,46 +397,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!(ok = warp_wait(&bars->dp_full, y))) break;
         tc::fence_after_sync();
-        uint32_t m[2] = {0xffffffffu, 0xffffffffu};
-        if (!all) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int t0 = key0 + c * 32;
-            m[c] = none ? 0u : bit_range(lo - t0, pos - t0) | bit_range(0, min(pos, p.sinks - 1) - t0);
-          }
-        }
-        const float2 nd2 = make_float2(-dd, -dd);
+        const float2 nd2 = make_float2(ndd, ndd);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t dv[32], dw[16];
-          tc::tmem_ld32(d_tm + c * 32, dv);
-          tc::tmem_wait_ld();
+          uint32_t dw[16];
+          if (none) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const int e = c * 32 + j;
-            const float2 ds = __fmul2_rn(make_float2(__uint_as_float(pf[e]), __uint_as_float(pf[e + 1])),
-                                         __fadd2_rn(make_float2(__uint_as_float(dv[j]), __uint_as_float(dv[j + 1])),
-                                                    nd2));
-            dw[j >> 1] = pack2<T>(ds.x, ds.y);
-          }
-          if (!all) {
-            // hidden pairs are cleared after the products: what they hold may not be finite
+            for (int j = 0; j < 16; ++j) dw[j] = 0u;
+          } else {
+            uint32_t dv[32];
+            tc::tmem_ld32(d_tm + c * 32, dv);
+            tc::tmem_wait_ld();
+            float2 ds[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              dw[j] &= (m[c] >> (2 * j) & 1u ? 0xffffu : 0u) | (m[c] >> (2 * j + 1) & 1u ? 0xffff0000u : 0u);
+            for (int j = 0; j < 16; ++j) {
+              const int e = c * 32 + 2 * j;
+              ds[j] = __fmul2_rn(
+                  make_float2(__uint_as_float(pf[e]), __uint_as_float(pf[e + 1])),
+                  __fadd2_rn(make_float2(__uint_as_float(dv[2 * j]), __uint_as_float(dv[2 * j + 1])), nd2));
+            }
+            if (!all) {
+              // hidden pairs are cleared after the products: what they hold may not be finite
+              const int t0 = key0 + c * 32;
+              const uint32_t seen = bit_range(lo - t0, pos - t0) | bit_range(0, min(pos, p.sinks - 1) - t0);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (!(seen & (1u << (2 * j)))) ds[j].x = 0.f;
+                if (!(seen & (2u << (2 * j)))) ds[j].y = 0.f;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dw[j] = pack2<T>(ds[j].x, ds[j].y);
           }
           tc::tmem_st16(d_tm + c * 16, dw);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->ds_full);
+        warp_arrive(&bars->ds_full, lane);
       }
       step += w.steps;
       x += 1 + 2 * w.steps;
       const int item = items++;
-      it.next();
-      seek(it);
-      const bool more = it.any();
       if (more) row_stats(it);  // (while the last dQ runs)
       if (!ok || !(ok = warp_wait(&bars->dq_full, item))) break;
       tc::fence_after_sync();
@@ -448,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_before_sync();
-      tc::mbar_arrive(&bars->dq_empty);
+      warp_arrive(&bars->dq_empty, lane);
     }
     if (!ok) raise_status(p.status, kTimeout, 333);
   }
@@ -489,7 +507,7 @@ struct KeyLayout {
   static constexpr int kChunk = 128 * 128, kTile = KC * kChunk;
   static constexpr int kOffK = 0, kOffV = kTile;
   static constexpr int kOffQ = 2 * kTile;              // [kNS] Q, dout
-  static constexpr int kOffInfo = kOffQ + kNS * 2 * kTile;  // [kNS] lse2[128], D[128]
+  static constexpr int kOffInfo = kOffQ + kNS * 2 * kTile;  // [kNS] -lse2[128], -D[128]
   static constexpr int kOffBar = kOffInfo + kNS * 1024;
   static constexpr int kAlloc = kOffBar + 256 + 1024;
 };
@@ -546,15 +564,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&bars->kv_empty, 1);
     for (int s = 0; s < kNS; ++s) {
       tc::mbar_init(&bars->q_full[s], 1);
-      tc::mbar_init(&bars->q_empty[s], 1 + kWorkers);
+      tc::mbar_init(&bars->q_empty[s], 1 + kWorkers / 32);
     }
     tc::mbar_init(&bars->tail, 1);
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->dp_full, 1);
-    for (int c = 0; c < 2; ++c) tc::mbar_init(&bars->p_full[c], kWorkers);
-    tc::mbar_init(&bars->ds_full, kWorkers);
+    for (int c = 0; c < 2; ++c) tc::mbar_init(&bars->p_full[c], kWorkers / 32);
+    tc::mbar_init(&bars->ds_full, kWorkers / 32);
     tc::mbar_init(&bars->acc_full, 1);
-    tc::mbar_init(&bars->acc_empty, kWorkers);
+    tc::mbar_init(&bars->acc_empty, kWorkers / 32);
     tc::mbar_init(&bars->drained, 1);
     tc::fence_barrier_init();
   }
@@ -608,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tma_load_4d(dst + L::kTile + kc * L::kChunk, &tm_do, bar, kc * 64, w.g * p.G, t * P, w.b);
           }
           const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + t) * kRows;
-          tc::bulk_load(smem + L::kOffInfo + st * 1024, p.lse2 + at, 512, bar);
-          tc::bulk_load(smem + L::kOffInfo + st * 1024 + 512, p.dd + at, 512, bar);
+          tc::bulk_load(smem + L::kOffInfo + st * 1024, p.nlse2 + at, 512, bar);
+          tc::bulk_load(smem + L::kOffInfo + st * 1024 + 512, p.ndd + at, 512, bar);
         }
         if (clear) {
           // p and dS are 0 there, but 0 x NaN is not
@@ -732,6 +750,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           m[1] = none ? 0u : bit_range(a - 32, b - 32);
         }
         const float2 sc2 = make_float2(sc, sc);
+        auto hand_over = [&](int c) {  // (the first part while the second is under way: its stores have ended by then)
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          warp_arrive(&bars->p_full[c], lane);
+        };
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pw[16];
@@ -745,9 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float4 l4 = *reinterpret_cast<const float4*>(info + c * 32 + j);
               const uint32_t* v = pf + c * 32 + j;
               y[0] = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), sc2,
-                                make_float2(-l4.x, -l4.y));
+                                make_float2(l4.x, l4.y));
               y[1] = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), sc2,
-                                make_float2(-l4.z, -l4.w));
+                                make_float2(l4.z, l4.w));
             };
             float2 y[2], next[2];
             scaled(0, y);
@@ -768,12 +791,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               y[1] = next[1];
               pw[j / 2] = pack2<T>(__uint_as_float(v[0]), __uint_as_float(v[1]));
               pw[j / 2 + 1] = pack2<T>(__uint_as_float(v[2]), __uint_as_float(v[3]));
+              if (c == 1 && j == 8) hand_over(0);
             }
           }
+          if (c == 1 && none) hand_over(0);
           tc::tmem_st16(s_tm + c * 16, pw);
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
-          tc::mbar_arrive(&bars->p_full[c]);
+          if (c == 1) hand_over(1);
         }
         // ---- dS^T
         if (!(ok = warp_wait(&bars->dp_full, q))) break;
@@ -790,10 +813,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = c * 32 + j;
             const float2 a = __fmul2_rn(make_float2(__uint_as_float(pf[e]), __uint_as_float(pf[e + 1])),
                                         __fadd2_rn(make_float2(__uint_as_float(dv[j]), __uint_as_float(dv[j + 1])),
-                                                   make_float2(-d4.x, -d4.y)));
+                                                   make_float2(d4.x, d4.y)));
             const float2 b = __fmul2_rn(make_float2(__uint_as_float(pf[e + 2]), __uint_as_float(pf[e + 3])),
                                         __fadd2_rn(make_float2(__uint_as_float(dv[j + 2]), __uint_as_float(dv[j + 3])),
-                                                   make_float2(-d4.z, -d4.w)));
+                                                   make_float2(d4.z, d4.w)));
             dw[j >> 1] = pack2<T>(a.x, a.y);
             dw[(j >> 1) + 1] = pack2<T>(b.x, b.y);
           }
@@ -801,8 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->ds_full);
-        tc::mbar_arrive(&bars->q_empty[st]);
+        warp_arrive(&bars->ds_full, lane);
+        warp_arrive(&bars->q_empty[st], lane);
       }
       if (!ok) break;
       // ---- dk, dv: each half of the workers takes half of the columns
@@ -855,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (any) {
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->acc_empty);
+        warp_arrive(&bars->acc_empty, lane);
       }
     }
     if (!ok) raise_status(p.status, kTimeout, 343);

@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars->q_full[t], 1);
       tc::mbar_init(&bars->q_empty[t], 1);
       tc::mbar_init(&bars->s_full[t], 1);
-      tc::mbar_init(&bars->p_full[t], kRows);
+      tc::mbar_init(&bars->p_full[t], kRows / 32);
       tc::mbar_init(&bars->o_full[t], 1);
-      tc::mbar_init(&bars->o_empty[t], kRows);
+      tc::mbar_init(&bars->o_empty[t], kRows / 32);
     }
     tc::fence_barrier_init();
   }
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         lsum = lsum * corr + lstep;
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->p_full[t]);
+        warp_arrive(&bars->p_full[t], lane);
       }
       if (!ok) break;
       // ---- the rows' output (zeros where there is no token) and log-sum-exp
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (w.steps > 0) {
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->o_empty[t]);
+        warp_arrive(&bars->o_empty[t], lane);
         step += w.steps;
         ++items;
       }

@@ -15,6 +15,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase) {
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, phase & 1));
 }
 
+// One arrival for a warp, after all of its lanes got here.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+
 // A CTA's work items x of (n_x per head, Hkv, B), x fastest: every gridDim.x-th
 // from blockIdx.x on.  The steps between them are kept as digits, so that the
 // way to the next item takes no division.
