@@ -1503,7 +1503,7 @@ struct WindowDecodeLayout {
 };
 WindowDecodeLayout window_decode_layout(int64_t G, int64_t D) {
   WindowDecodeLayout L{};
-  L.n_cta = num_sms();
+  L.n_cta = std::min(num_sms(), dash::kMaxDecodeCtas);
   L.status = 0;
   L.cta_status = align256(sizeof(dash::DeviceStatus));
   L.part_o = align256(L.cta_status + (size_t)L.n_cta * 4);

@@ -76,6 +76,7 @@ cudaError_t launch_window_fwd_simt(const WindowParams& p, cudaStream_t stream);
 cudaError_t launch_window_bwd_simt(const WindowParams& p, cudaStream_t stream);
 
 // ---------------------------------------------------------------- decode
+constexpr int kMaxDecodeCtas = 256;  // streaming CTAs: one per SM
 struct WindowDecodeParams {
   View q, k, v, out;           // q, out [B, 1, H, D]; k, v [B, Lmax, Hkv, D] or pages [n_pages, block, Hkv, D]
   int dtype;

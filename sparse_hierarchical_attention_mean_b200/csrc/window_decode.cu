@@ -409,10 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // One CTA per (KV head, sequence): merges the partials of a divided one in
 // order, writes zeros for a sequence without tokens; the first CTA also
-// writes the status word.
+// writes the status word.  Bound by latency: the weights of all parts first (a
+// warp per head), then the outputs, whose loads depend on nothing.
+constexpr int kJoinThreads = 256;
 template <typename T>
-__global__ void __launch_bounds__(128) window_decode_join_kernel(const WindowDecodeParams p) {
-  const int g = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kJoinThreads) window_decode_join_kernel(const WindowDecodeParams p) {
+  __shared__ float weight[kMaxDecodeCtas][8];  // of part i for head h, 1 / l included
+  const int g = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.G, D = p.D;
   long long total, before;
   batch_steps(p, b, lane, &total, &before);
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(128) window_decode_join_kernel(const WindowDec
   const Cut cut(total * p.Hkv, p.n_cta);
   const long long u0 = before * p.Hkv + (long long)g * q.n;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  if (g == 0 && b == 0 && threadIdx.x < 32) {
+  if (g == 0 && b == 0 && warp == 0) {
     int code = 0;
     for (int c = lane; c < p.n_cta; c += 32) code = max(code, p.cta_status[c]);
     for (int i = lane; i < p.B; i += 32)
@@ -434,36 +437,43 @@ __global__ void __launch_bounds__(128) window_decode_join_kernel(const WindowDec
   }
   T* dst = static_cast<T*>(const_cast<void*>(p.out.data)) + (int64_t)b * p.out.sb + (int64_t)g * G * p.out.sh;
   if (q.n == 0) {
-    for (int e = threadIdx.x * 2; e < G * D; e += 256) {
+    for (int e = threadIdx.x * 2; e < G * D; e += kJoinThreads * 2) {
       *reinterpret_cast<uint32_t*>(dst + (int64_t)(e / D) * p.out.sh + e % D) = 0u;
       if (p.lse && e % D == 0) p.lse[(int64_t)b * p.H + g * G + e / D] = kNegInf;
     }
     return;
   }
-  const int c0 = cut.owner(u0), c1 = cut.owner(u0 + q.n - 1);
-  if (c0 == c1) return;  // finished by its CTA
-  for (int e = threadIdx.x * 2; e < G * D; e += 256) {
-    const int h = e / D, c = e % D;
-    float M = kNegInf;
-    for (int u = c0; u <= c1; ++u) {
-      const int64_t slot = 2 * (int64_t)u + (u == c0 ? 1 : 0);
-      M = fmaxf(M, p.part_ml[(slot * G + h) * 2]);
-    }
-    const float Mu = M == kNegInf ? 0.f : M;
-    float a0 = 0.f, a1 = 0.f, sum = 0.f;
-    for (int u = c0; u <= c1; ++u) {
-      const int64_t slot = 2 * (int64_t)u + (u == c0 ? 1 : 0);
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * G + h) * 2);
-      const float2 ov = *reinterpret_cast<const float2*>(p.part_o + (slot * G + h) * D + c);
+  const int c0 = cut.owner(u0), parts = cut.owner(u0 + q.n - 1) - c0 + 1;
+  if (parts == 1) return;  // finished by its CTA
+  // part i lies in the second slot of the first CTA, then in the first slot of the others
+  auto slot = [&](int i) { return 2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0); };
+  if (warp < G) {
+    float m = kNegInf, l = 0.f;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[(slot(i) * G + warp) * 2]);
+    const float M = warp_max(m), Mu = M == kNegInf ? 0.f : M;
+    for (int i = lane; i < parts; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(i) * G + warp) * 2);
       const float f = tc::ex2(ml.x - Mu);
-      a0 = fmaf(f, ov.x, a0);
-      a1 = fmaf(f, ov.y, a1);
-      sum = fmaf(f, ml.y, sum);
+      weight[i][warp] = f;
+      l = fmaf(f, ml.y, l);
     }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    *reinterpret_cast<uint32_t*>(dst + (int64_t)h * p.out.sh + c) = pack2<T>(a0 * inv, a1 * inv);
-    if (p.lse && c == 0)
-      p.lse[(int64_t)b * p.H + g * G + h] = sum == 0.f ? kNegInf : (M + log2f(sum)) / kLog2e;
+    l = warp_sum(l);
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+    for (int i = lane; i < parts; i += 32) weight[i][warp] *= inv;
+    if (p.lse && lane == 0) p.lse[(int64_t)b * p.H + g * G + warp] = l == 0.f ? kNegInf : (M + log2f(l)) / kLog2e;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x * 2; e < G * D; e += kJoinThreads * 2) {
+    const int h = e / D, c = e % D;
+    const float* src = p.part_o + (int64_t)h * D + c;
+    float a0 = 0.f, a1 = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) {
+      const float2 ov = *reinterpret_cast<const float2*>(src + slot(i) * G * D);
+      a0 = fmaf(weight[i][h], ov.x, a0);
+      a1 = fmaf(weight[i][h], ov.y, a1);
+    }
+    *reinterpret_cast<uint32_t*>(dst + (int64_t)h * p.out.sh + c) = pack2<T>(a0, a1);
   }
 }
 
@@ -472,8 +482,11 @@ cudaError_t run(const WindowDecodeParams& p, cudaStream_t stream) {
   using L = Layout<D>;
   CUtensorMap mk, mv;
   const int64_t rows = p.block_table ? p.block : p.Lmax, outer = p.block_table ? p.n_pages : p.B;
-  if (!make_map(&mk, p.k, p.dtype, outer, rows, p.Hkv, D, 1, kStep) ||
-      !make_map(&mv, p.v, p.dtype, outer, rows, p.Hkv, D, 1, kStep))
+  // D = 64: a token's 128 bytes of one KV head.  With 256-byte fetches the
+  // next head's came too and were gone again before their turn: 705 MB read
+  // for 537 (16 sequences of up to 16K tokens, 16 KV heads).
+  if (!make_map(&mk, p.k, p.dtype, outer, rows, p.Hkv, D, 1, kStep, D == 64) ||
+      !make_map(&mv, p.v, p.dtype, outer, rows, p.Hkv, D, 1, kStep, D == 64))
     return cudaErrorInvalidValue;
   auto kern = window_decode_kernel<T, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
@@ -483,7 +496,7 @@ cudaError_t run(const WindowDecodeParams& p, cudaStream_t stream) {
   // the join's launch overlaps the streaming kernel's end; it waits for its results itself
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.Hkv, p.B);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
