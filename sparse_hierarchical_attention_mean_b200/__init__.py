@@ -751,7 +751,7 @@ def window_fwd(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor |
         B, S, H, _ = q.shape
         out = torch.empty_like(q) if out is None else out
         if return_lse and lse is None:
-            lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, H, S), dtype=torch.float32)
         ws, room = _scratch(_lib.dash_attn_window_fwd_workspace_size(qd, kd), "dash_attn_window_fwd_workspace_size",
                             q.device, workspace)
         _check(_lib.dash_attn_window_fwd(qd, kd, _packed(v), _array(seqlens, "seqlens", (B,)), window, sinks,
@@ -827,7 +827,7 @@ def _window_decode(q, k, v, table, seqlens, window, sinks, out, return_lse, lse,
         B, _, H, d = q.shape
         out = torch.empty_like(q) if out is None else out
         if return_lse and lse is None:
-            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, H), dtype=torch.float32)
         ws, room = _scratch(_lib.dash_attn_window_decode_workspace_size(H, k.shape[2], d),
                             "dash_attn_window_decode_workspace_size", q.device, workspace)
         tail = (_array(seqlens, "seqlens", (B,)), window, sinks, _packed(out),
@@ -893,7 +893,7 @@ def pages_grow(block_table, seqlens, refs, n_new, block: int, workspace=None, st
     with _On(stream, block_table, seqlens, refs, n_new, workspace) as s:
         state = _pages_state(block_table, seqlens, refs)
         batch = state[1]
-        src, dst = torch.empty((2, batch), dtype=torch.int32, device=block_table.device).unbind()
+        src, dst = torch.empty_like(n_new), torch.empty_like(n_new)
         ws, room = _pages_scratch(state, block_table.device, workspace)
         _check(_lib.dash_attn_pages_grow(*state, _array(n_new, "n_new", (batch,)), block, src.data_ptr(),
                                          dst.data_ptr(), ws.data_ptr(), room, s))
@@ -911,8 +911,7 @@ def pages_compact(block_table, seqlens, refs, block: int, inplace: bool = False,
         dev, n_pages = block_table.device, state[5]
         table_out = block_table if inplace else torch.empty_like(block_table)
         refs_out = refs if inplace else torch.empty_like(refs)
-        src, dst = torch.empty((2, n_pages // 2), dtype=torch.int32, device=dev).unbind()
-        info = torch.empty(2, dtype=torch.int32, device=dev)
+        src, dst, info = (refs.new_empty(n) for n in (n_pages // 2, n_pages // 2, 2))
         ws, room = _pages_scratch(state, dev, workspace)
         _check(_lib.dash_attn_pages_compact(*state, block, table_out.data_ptr(), refs_out.data_ptr(), src.data_ptr(),
                                             dst.data_ptr(), info.data_ptr(), ws.data_ptr(), room, s))

@@ -27,19 +27,16 @@ constexpr int ld() {
   return D + 4;
 }
 
-template <typename T, int D>
+// Starts the copies of a tile (16 bytes each; rows at or past n as zeros); the
+// caller commits and waits for them.
+template <int D>
 __device__ __forceinline__ void load_tile(float* dst, const View& v, int b, int h, int row0, int n) {
-  constexpr int P = Elt<T>::kPerVec, V = D / P;
-  const T* src = static_cast<const T*>(v.data) + (int64_t)b * v.sb + (int64_t)h * v.sh;
+  constexpr int V = D / 4;
+  const float* src = static_cast<const float*>(v.data) + (int64_t)b * v.sb + (int64_t)h * v.sh;
   for (int i = threadIdx.x; i < kT * V; i += kThreads) {
-    const int r = i / V, c = (i % V) * P;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (row0 + r < n) x = *reinterpret_cast<const uint4*>(src + (int64_t)(row0 + r) * v.ss + c);
-    float f[P];
-    Elt<T>::to_float(x, f);
-#pragma unroll
-    for (int e = 0; e < P; e += 4)
-      *reinterpret_cast<float4*>(dst + r * ld<D>() + c + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    const int r = i / V, c = (i % V) * 4;
+    const bool there = row0 + r < n;
+    cp_async16(dst + r * ld<D>() + c, src + (int64_t)(there ? row0 + r : 0) * v.ss + c, there);
   }
 }
 
@@ -92,26 +89,19 @@ __device__ __forceinline__ void add_product(const float* w, const float* m, int 
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* dst, float a, float b, float c, float d) {
-  if constexpr (sizeof(T) == 4)
-    *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
-  else
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(a, b), pack2<T>(c, d));
-}
-
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void store_rows(const View& v, int b, int h, int row0, int S, int ty, int tx,
                                            const float (&acc)[4][D / 16], const float (&scale)[4]) {
-  T* dst = static_cast<T*>(const_cast<void*>(v.data)) + (int64_t)b * v.sb + (int64_t)h * v.sh;
+  float* dst = static_cast<float*>(const_cast<void*>(v.data)) + (int64_t)b * v.sb + (int64_t)h * v.sh;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = row0 + 4 * ty + i;
     if (r >= S) continue;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
-      store4<T>(dst + (int64_t)r * v.ss + 4 * tx + 64 * j, acc[i][4 * j] * scale[i], acc[i][4 * j + 1] * scale[i],
-                acc[i][4 * j + 2] * scale[i], acc[i][4 * j + 3] * scale[i]);
+      *reinterpret_cast<float4*>(dst + (int64_t)r * v.ss + 4 * tx + 64 * j) =
+          make_float4(acc[i][4 * j] * scale[i], acc[i][4 * j + 1] * scale[i], acc[i][4 * j + 2] * scale[i],
+                      acc[i][4 * j + 3] * scale[i]);
   }
 }
 
@@ -137,7 +127,7 @@ constexpr int tile_floats() {
 }
 constexpr int kScoreFloats = kT * (kT + 4);
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(WindowParams p) {
   extern __shared__ __align__(16) float smem[];
   float* qs = smem;
@@ -159,16 +149,23 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(WindowParams 
   }
   if (r0 < n) {
     const float scale = rsqrtf((float)D) * kLog2e;
-    load_tile<T, D>(qs, p.q, b, h, r0, n);
     const KeyTiles kt(r0, min(r0 + kT, n), p.window, p.sinks, kT);
+    // K of the next tile comes during this one's softmax and second product, V
+    // of it during its first
+    load_tile<D>(qs, p.q, b, h, r0, n);
+    load_tile<D>(ks, p.k, b, g, kt.tile(0) * kT, n);
+    cp_async_commit();
+    load_tile<D>(vs, p.v, b, g, kt.tile(0) * kT, n);
+    cp_async_commit();
     for (int t = 0; t < kt.n; ++t) {
-      const int k0 = kt.tile(t) * kT;
-      __syncthreads();
-      load_tile<T, D>(ks, p.k, b, g, k0, n);
-      load_tile<T, D>(vs, p.v, b, g, k0, n);
+      const int k0 = kt.tile(t) * kT, k1 = t + 1 < kt.n ? kt.tile(t + 1) * kT : p.S;  // p.S: nothing to load
+      cp_async_wait<1>();
       __syncthreads();
       float s[4][4];
       dot_tile<D>(qs, ks, ty, tx, s);
+      __syncthreads();
+      load_tile<D>(ks, p.k, b, g, k1, min(n, k1 + kT));
+      cp_async_commit();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float mx = kNegInf;
@@ -192,9 +189,14 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(WindowParams 
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) acc[i][j] *= corr;
       }
-      __syncwarp();  // a row of ps is written and read by the same half warp
+      cp_async_wait<1>();
+      __syncthreads();
       add_product<D>(ps, vs, ty, tx, acc);
+      __syncthreads();
+      load_tile<D>(vs, p.v, b, g, k1, min(n, k1 + kT));
+      cp_async_commit();
     }
+    cp_async_wait<0>();
   }
   float inv[4];
 #pragma unroll
@@ -204,11 +206,11 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(WindowParams 
     if (p.lse && tx == 0 && r < p.S)
       p.lse[((int64_t)b * p.H + h) * p.S + r] = l[i] > 0.f ? m[i] / kLog2e + logf(l[i]) : kNegInf;
   }
-  store_rows<T, D>(p.out, b, h, r0, p.S, ty, tx, acc, inv);
+  store_rows<D>(p.out, b, h, r0, p.S, ty, tx, acc, inv);
 }
 
 // One 64-row tile of one head: D_i (written for the key kernel) and dq.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_bwd_row_simt_kernel(WindowParams p) {
   extern __shared__ __align__(16) float smem[];
   float* qs = smem;
@@ -230,9 +232,11 @@ __global__ void __launch_bounds__(kThreads) window_bwd_row_simt_kernel(WindowPar
   }
   if (r0 < n) {
     const float scale = rsqrtf((float)D) * kLog2e;
-    load_tile<T, D>(qs, p.q, b, h, r0, n);
-    load_tile<T, D>(dos, p.dout, b, h, r0, n);
-    load_tile<T, D>(ks, p.out, b, h, r0, n);
+    load_tile<D>(qs, p.q, b, h, r0, n);
+    load_tile<D>(dos, p.dout, b, h, r0, n);
+    load_tile<D>(ks, p.out, b, h, r0, n);
+    cp_async_commit();
+    cp_async_wait<0>();
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -247,8 +251,10 @@ __global__ void __launch_bounds__(kThreads) window_bwd_row_simt_kernel(WindowPar
     for (int t = 0; t < kt.n; ++t) {
       const int k0 = kt.tile(t) * kT;
       __syncthreads();
-      load_tile<T, D>(ks, p.k, b, g, k0, n);
-      load_tile<T, D>(vs, p.v, b, g, k0, n);
+      load_tile<D>(ks, p.k, b, g, k0, n);
+      load_tile<D>(vs, p.v, b, g, k0, n);
+      cp_async_commit();
+      cp_async_wait<0>();
       __syncthreads();
       float s[4][4], dp[4][4];
       dot_tile<D>(qs, ks, ty, tx, s);
@@ -265,12 +271,12 @@ __global__ void __launch_bounds__(kThreads) window_bwd_row_simt_kernel(WindowPar
       add_product<D>(dss, ks, ty, tx, acc);
     }
   }
-  store_rows<T, D>(p.dq, b, h, r0, p.S, ty, tx, acc, one);
+  store_rows<D>(p.dq, b, h, r0, p.S, ty, tx, acc, one);
 }
 
 // One 64-key tile of one KV head: dk and dv, summed over the group's heads in
 // order and over the row tiles in order (no atomics: the same every time).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_bwd_key_simt_kernel(WindowParams p) {
   extern __shared__ __align__(16) float smem[];
   float* ks = smem;
@@ -292,8 +298,8 @@ __global__ void __launch_bounds__(kThreads) window_bwd_key_simt_kernel(WindowPar
   }
   if (k0 < n) {
     const float scale = rsqrtf((float)D) * kLog2e;
-    load_tile<T, D>(ks, p.k, b, g, k0, n);
-    load_tile<T, D>(vs, p.v, b, g, k0, n);
+    load_tile<D>(ks, p.k, b, g, k0, n);
+    load_tile<D>(vs, p.v, b, g, k0, n);
     // the last row that sees a key of the tile (every later row when it holds sinks)
     const int last = k0 < p.sinks ? n - 1 : (int)min((int64_t)n - 1, (int64_t)k0 + kT - 1 + p.window - 1);
     for (int gh = 0; gh < p.G; ++gh) {
@@ -301,8 +307,10 @@ __global__ void __launch_bounds__(kThreads) window_bwd_key_simt_kernel(WindowPar
       const int64_t rbase = ((int64_t)b * p.H + h) * p.S;
       for (int r0 = k0; r0 <= last; r0 += kT) {
         __syncthreads();
-        load_tile<T, D>(qs, p.q, b, h, r0, n);
-        load_tile<T, D>(dos, p.dout, b, h, r0, n);
+        load_tile<D>(qs, p.q, b, h, r0, n);
+        load_tile<D>(dos, p.dout, b, h, r0, n);
+        cp_async_commit();
+        cp_async_wait<0>();
         __syncthreads();
         float s[4][4], dp[4][4];
         dot_tile<D>(ks, qs, ty, tx, s);
@@ -331,8 +339,8 @@ __global__ void __launch_bounds__(kThreads) window_bwd_key_simt_kernel(WindowPar
       }
     }
   }
-  store_rows<T, D>(p.dk, b, g, k0, p.S, ty, tx, dk, sk);
-  store_rows<T, D>(p.dv, b, g, k0, p.S, ty, tx, dv, sv);
+  store_rows<D>(p.dk, b, g, k0, p.S, ty, tx, dk, sk);
+  store_rows<D>(p.dv, b, g, k0, p.S, ty, tx, dv, sv);
 }
 
 template <typename K>
@@ -343,35 +351,28 @@ cudaError_t launch(K kern, dim3 grid, int floats, const WindowParams& p, cudaStr
   return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run_fwd(const WindowParams& p, cudaStream_t stream) {
-  return launch(window_fwd_simt_kernel<T, D>, dim3((p.S + kT - 1) / kT, p.H, p.B),
+  return launch(window_fwd_simt_kernel<D>, dim3((p.S + kT - 1) / kT, p.H, p.B),
                 3 * tile_floats<D>() + kScoreFloats, p, stream);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run_bwd(const WindowParams& p, cudaStream_t stream) {
   const unsigned tiles = (p.S + kT - 1) / kT;
   const int floats = 4 * tile_floats<D>() + kScoreFloats;
-  cudaError_t e = launch(window_bwd_row_simt_kernel<T, D>, dim3(tiles, p.H, p.B), floats, p, stream);
+  cudaError_t e = launch(window_bwd_row_simt_kernel<D>, dim3(tiles, p.H, p.B), floats, p, stream);
   if (e != cudaSuccess) return e;
-  return launch(window_bwd_key_simt_kernel<T, D>, dim3(tiles, p.Hkv, p.B), floats, p, stream);
-}
-
-template <typename T>
-cudaError_t run(const WindowParams& p, bool bwd, cudaStream_t stream) {
-  if (p.D == 128) return bwd ? run_bwd<T, 128>(p, stream) : run_fwd<T, 128>(p, stream);
-  return bwd ? run_bwd<T, 64>(p, stream) : run_fwd<T, 64>(p, stream);
-}
-
-cudaError_t run(const WindowParams& p, bool bwd, cudaStream_t stream) {
-  if (p.dtype == 0) return run<float>(p, bwd, stream);
-  return p.dtype == 1 ? run<__half>(p, bwd, stream) : run<__nv_bfloat16>(p, bwd, stream);
+  return launch(window_bwd_key_simt_kernel<D>, dim3(tiles, p.Hkv, p.B), floats, p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_window_fwd_simt(const WindowParams& p, cudaStream_t stream) { return run(p, false, stream); }
-cudaError_t launch_window_bwd_simt(const WindowParams& p, cudaStream_t stream) { return run(p, true, stream); }
+cudaError_t launch_window_fwd_simt(const WindowParams& p, cudaStream_t stream) {
+  return p.D == 128 ? run_fwd<128>(p, stream) : run_fwd<64>(p, stream);
+}
+cudaError_t launch_window_bwd_simt(const WindowParams& p, cudaStream_t stream) {
+  return p.D == 128 ? run_bwd<128>(p, stream) : run_bwd<64>(p, stream);
+}
 
 }  // namespace dash
