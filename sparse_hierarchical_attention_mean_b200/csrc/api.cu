@@ -1506,9 +1506,10 @@ WindowDecodeLayout window_decode_layout(int64_t G, int64_t D) {
   L.n_cta = std::min(num_sms(), dash::kMaxDecodeCtas);
   L.status = 0;
   L.cta_status = align256(sizeof(dash::DeviceStatus));
+  const int64_t heads = D == 64 ? 2 * G : G;  // query heads of a unit: 64-wide KV heads may go in pairs
   L.part_o = align256(L.cta_status + (size_t)L.n_cta * 4);
-  L.part_ml = align256(L.part_o + (size_t)2 * L.n_cta * G * D * 4);
-  L.total = align256(L.part_ml + (size_t)2 * L.n_cta * G * 2 * 4);
+  L.part_ml = align256(L.part_o + (size_t)2 * L.n_cta * heads * D * 4);
+  L.total = align256(L.part_ml + (size_t)2 * L.n_cta * heads * 2 * 4);
   return L;
 }
 

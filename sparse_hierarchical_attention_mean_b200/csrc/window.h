@@ -91,9 +91,10 @@ struct WindowDecodeParams {
   // workspace
   DeviceStatus* status;
   int32_t* cta_status;         // [n_cta] what each streaming CTA saw (0: nothing wrong)
-  float* part_o;               // [2 n_cta, G, D] unnormalised partial outputs
-  float* part_ml;              // [2 n_cta, G, 2] their reference max (log2 units) and sum
+  float* part_o;               // [2 n_cta, heads of a unit, D] unnormalised partial outputs
+  float* part_ml;              // [2 n_cta, heads of a unit, 2] their reference max (log2 units) and sum
   int n_cta;
+  int units;                   // KV heads, or pairs of them, of a sequence (set by the launch)
 };
 cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream);
 

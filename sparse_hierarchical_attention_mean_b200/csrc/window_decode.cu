@@ -16,6 +16,9 @@
 // partial (o, m, l) per CTA, at most two per CTA, and the join kernel merges
 // them in order (the result does not depend on timing).
 //
+// With 64-wide heads a unit takes two adjacent KV heads (HP = 2), two consumer
+// warps each: one head's 128 bytes of a token at a time reached 4.4 TB/s.
+//
 // G <= 8 query heads are the rows of a warp-level m16n8k16 MMA (half of it is
 // padding: the products need 1% of the tensor rate, the 64-row minimum of
 // tcgen05 would waste eight times that).  P is rounded to the cache's type
@@ -28,6 +31,7 @@
 // (only in the steps that hold a mask's edge), so NaN there is harmless.
 #include <cuda.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -43,12 +47,12 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kMinUnits = 2;  // steps a CTA takes at least, before more CTAs share the work
 
-template <int D>
+template <int D, int HP>
 struct Layout {
-  static constexpr int KC = D / 64;
+  static constexpr int KC = HP * D / 64;             // 64-column chunks of a token
   static constexpr int kChunk = kStep * 128;         // 64 tokens x 128 bytes
   static constexpr int kTile = KC * kChunk;          // K (or V) of a step
-  static constexpr int kStages = D == 128 ? 6 : 12;  // 192 KB in flight per SM
+  static constexpr int kStages = 12 / KC;            // 192 KB in flight per SM
   static constexpr int kOffO = 2 * kStages * kTile;  // merge buffer [4][8][D] fp32
   static constexpr int kOffMl = kOffO + kConsumers * 8 * D * 4;
   static constexpr int kOffBar = kOffMl + kConsumers * 8 * 2 * 4;
@@ -107,7 +111,8 @@ struct Cut {
   __device__ int owner(long long u) const { return (int)(((u + 1) * n - 1) / units); }
 };
 
-// Walks a part of the line: the (sequence, KV head) segments in order.
+// Walks a part of the line: the (sequence, KV head or pair of them) segments in
+// order.
 struct Walk {
   int b, g, s0, s1;    // segment: steps [s0, s1) of (b, g)
   bool whole;          // the segment is all of (b, g)
@@ -120,7 +125,7 @@ struct Walk {
     // the sequence that holds step u
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const long long n = (long long)lane_steps(p, b0, lane) * p.Hkv;
+      const long long n = (long long)lane_steps(p, b0, lane) * p.units;
       long long inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -131,7 +136,7 @@ struct Walk {
       if (hit) {
         const int w = __ffs(hit) - 1;
         const long long first = base + __shfl_sync(0xffffffffu, inc - n, w);
-        const int steps = (int)(__shfl_sync(0xffffffffu, n, w) / p.Hkv);
+        const int steps = (int)(__shfl_sync(0xffffffffu, n, w) / p.units);
         b = b0 + w;
         g = (int)((u - first) / steps);
         s0 = (int)((u - first) % steps);
@@ -151,7 +156,7 @@ struct Walk {
     left -= s1 - s0;
     if (left <= 0) return false;
     s0 = 0;
-    if (++g == p.Hkv) {
+    if (++g == p.units) {
       g = 0;
       do {
         ++b;
@@ -162,14 +167,16 @@ struct Walk {
   }
 };
 
-template <typename T, int D>
+template <typename T, int D, int HP>
 __global__ void __launch_bounds__(kThreads, 1)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const WindowDecodeParams p) {
-  using L = Layout<D>;
+  using L = Layout<D, HP>;
   constexpr int kStages = L::kStages;
-  constexpr int KS = D / 16;  // k slices of S = Q K^T
-  constexpr int NT = D / 8;   // 8-wide tiles of O
+  constexpr int KS = D / 16;             // k slices of S = Q K^T
+  constexpr int NT = D / 8;              // 8-wide tiles of O
+  constexpr int kShare = kConsumers / HP;  // warps of a KV head
+  constexpr int TG = kStep / kShare / 16;  // 16-token groups of a warp in a step
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* obuf = reinterpret_cast<float*>(smem + L::kOffO);
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   long long total;
   batch_steps(p, 0, lane, &total, nullptr);
-  const Cut cut(total * p.Hkv, p.n_cta);
+  const Cut cut(total * p.units, p.n_cta);
   Walk w;
   const bool any = total > 0 && w.begin(p, cut, blockIdx.x, lane);
 
@@ -233,8 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kc = 0; kc < L::KC; ++kc) {
             uint8_t* dst = smem + st * 2 * L::kTile + kc * L::kChunk;
-            tc::tma_load_4d(dst, &tm_k, &full[st], kc * 64, w.g, c2, c3);
-            tc::tma_load_4d(dst + L::kTile, &tm_v, &full[st], kc * 64, w.g, c2, c3);
+            const int col = HP == 2 ? 0 : kc * 64, head = HP == 2 ? w.g * 2 + kc : w.g;
+            tc::tma_load_4d(dst, &tm_k, &full[st], col, head, c2, c3);
+            tc::tma_load_4d(dst + L::kTile, &tm_v, &full[st], col, head, c2, c3);
           }
         }
         ++i;
@@ -246,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (any) {
     // ------------------------------------------------------------ consumers
     const int G = p.G, gq = lane >> 2, tq = lane & 3;
+    const int hs = warp / kShare, tok_w = warp % kShare * TG * 16;  // KV head of the unit, first token of a step
     const float qk_scale = rsqrtf((float)D) * kLog2e;
     SeqSteps q(p, w.b);
     int i = 0;
@@ -255,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A fragments of the query heads (rows gq >= G and 8..15 are zero)
       uint32_t qa[KS][2];
       {
-        const T* src = static_cast<const T*>(p.q.data) + (int64_t)w.b * p.q.sb + (int64_t)(w.g * G + gq) * p.q.sh;
+        const T* src = static_cast<const T*>(p.q.data) + (int64_t)w.b * p.q.sb + (int64_t)((w.g * HP + hs) * G + gq) * p.q.sh;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
           qa[kk][0] = gq < G ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * tq) : 0u;
@@ -273,42 +282,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&full[st], (i / kStages) & 1));
         if (!ok) break;
         const uint32_t kst = smem_u32(smem + st * 2 * L::kTile), vst = kst + L::kTile;
-        // S = Q K^T of this warp's 16 tokens
-        float sacc[2][4];
+        const int mt = lane >> 3, rr = lane & 7;
+        // S = Q K^T of this warp's tokens, 8 a tile
+        float sacc[2 * TG][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) sacc[n][0] = sacc[n][1] = sacc[n][2] = sacc[n][3] = 0.f;
-        {
-          const int mt = lane >> 3, rr = lane & 7;
-          const int row = warp * 16 + (mt >> 1) * 8 + rr;
+        for (int n = 0; n < 2 * TG; ++n) sacc[n][0] = sacc[n][1] = sacc[n][2] = sacc[n][3] = 0.f;
 #pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-            const int c = 2 * (kk & 3) + (mt & 1);
+        for (int kk = 0; kk < KS; ++kk) {
+          const int c = 2 * (kk & 3) + (mt & 1), chunk = HP == 2 ? hs : kk >> 2;
+          const uint32_t a[4] = {qa[kk][0], 0u, qa[kk][1], 0u};
+#pragma unroll
+          for (int t = 0; t < TG; ++t) {
+            const int row = tok_w + t * 16 + (mt >> 1) * 8 + rr;
             uint32_t bf[4];
-            ldsm_x4(kst + (kk >> 2) * L::kChunk + row * 128 + ((c ^ (row & 7)) << 4), bf);
-            const uint32_t a[4] = {qa[kk][0], 0u, qa[kk][1], 0u};
-            mma16816<T>(sacc[0], a, bf[0], bf[1]);
-            mma16816<T>(sacc[1], a, bf[2], bf[3]);
+            ldsm_x4(kst + chunk * L::kChunk + row * 128 + ((c ^ (row & 7)) << 4), bf);
+            mma16816<T>(sacc[2 * t], a, bf[0], bf[1]);
+            mma16816<T>(sacc[2 * t + 1], a, bf[2], bf[3]);
           }
         }
-        // logits of head gq (log2 units) for tokens 2tq, 2tq + 1, 8 + 2tq, 9 + 2tq
+        // logits of head gq (log2 units) for tokens 8 n + 2 tq and the next one
         const int tok0 = q.tok0(s);
         const bool edge = tok0 + kStep > q.L || tok0 < q.lo;  // some token of the step may be hidden
-        float x[4];
-        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+        uint32_t vm[2 * TG];
+        float mx = kNegInf;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = sacc[e >> 1][e & 1] * qk_scale;
-        if (edge) {
-          bool seen[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = tok0 + warp * 16 + (e >> 1) * 8 + 2 * tq + (e & 1);
-            seen[e] = t < q.L && (t >= q.lo || t < p.sinks);
-            if (!seen[e]) x[e] = kNegInf;
+        for (int n = 0; n < 2 * TG; ++n) {
+          vm[n] = 0xffffffffu;
+          sacc[n][0] *= qk_scale;
+          sacc[n][1] *= qk_scale;
+          if (edge) {
+            const int t = tok0 + tok_w + n * 8 + 2 * tq;
+            const bool s0 = t < q.L && (t >= q.lo || t < p.sinks);
+            const bool s1 = t + 1 < q.L && (t + 1 >= q.lo || t + 1 < p.sinks);
+            if (!s0) sacc[n][0] = kNegInf;
+            if (!s1) sacc[n][1] = kNegInf;
+            vm[n] = (s0 ? 0xffffu : 0u) | (s1 ? 0xffff0000u : 0u);
           }
-          vm0 = (seen[0] ? 0xffffu : 0u) | (seen[1] ? 0xffff0000u : 0u);
-          vm1 = (seen[2] ? 0xffffu : 0u) | (seen[3] ? 0xffff0000u : 0u);
+          mx = fmaxf(mx, fmaxf(sacc[n][0], sacc[n][1]));
         }
-        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         float corr = 1.0f;
@@ -330,25 +341,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           lpart *= corr;
         }
-        float pe[4];
+        const float off = m_used == kNegInf ? 0.f : m_used;
+        uint32_t pw[2 * TG];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pe[e] = m_used == kNegInf ? 0.f : tc::ex2(x[e] - m_used);
-        lpart += (pe[0] + pe[1]) + (pe[2] + pe[3]);
-        const uint32_t pa[4] = {pack2<T>(pe[0], pe[1]), 0u, pack2<T>(pe[2], pe[3]), 0u};
+        for (int n = 0; n < 2 * TG; ++n) {
+          const float e0 = tc::ex2(sacc[n][0] - off), e1 = tc::ex2(sacc[n][1] - off);
+          lpart += e0 + e1;
+          pw[n] = pack2<T>(e0, e1);
+        }
         // O += P V
-        {
-          const int mt = lane >> 3, rr = lane & 7;
-          const int row = warp * 16 + (mt & 1) * 8 + rr;
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+          const uint32_t pa[4] = {pw[2 * t], 0u, pw[2 * t + 1], 0u};
+          const int row = tok_w + t * 16 + (mt & 1) * 8 + rr;
 #pragma unroll
           for (int j = 0; j < NT / 2; ++j) {
-            const int c = 2 * j + (mt >> 1);
+            const int c = 2 * j + (mt >> 1), chunk = HP == 2 ? hs : c >> 3;
             uint32_t bf[4];
-            ldsm_x4_t(vst + (c >> 3) * L::kChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4), bf);
+            ldsm_x4_t(vst + chunk * L::kChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4), bf);
             if (edge) {
-              bf[0] &= vm0;
-              bf[1] &= vm1;
-              bf[2] &= vm0;
-              bf[3] &= vm1;
+              bf[0] &= vm[2 * t];
+              bf[1] &= vm[2 * t + 1];
+              bf[2] &= vm[2 * t];
+              bf[3] &= vm[2 * t + 1];
             }
             mma16816<T>(o[2 * j], pa, bf[0], bf[1]);
             mma16816<T>(o[2 * j + 1], pa, bf[2], bf[3]);
@@ -357,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&empty[st]);
       }
-      // merge the four warps
+      // merge the warps of each KV head
       float l = lpart;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -372,31 +387,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       asm volatile("bar.sync 1, %0;\n" ::"n"(kConsumers * 32) : "memory");
       const int64_t slot = 2 * (int64_t)blockIdx.x + (w.head ? 0 : 1);
-      for (int e = threadIdx.x * 2; e < G * D; e += kConsumers * 64) {
-        const int h = e / D, c = e % D;
+      for (int e = threadIdx.x * 2; e < HP * G * D; e += kConsumers * 64) {
+        const int uh = e / D, c = e % D;  // query head of the unit
+        const bool second = HP == 2 && uh >= G;
+        const int w0 = second ? kShare : 0, h = second ? uh - G : uh;
         float M = kNegInf;
 #pragma unroll
-        for (int u = 0; u < kConsumers; ++u) M = fmaxf(M, mlbuf[(u * 8 + h) * 2]);
+        for (int u = 0; u < kShare; ++u) M = fmaxf(M, mlbuf[((w0 + u) * 8 + h) * 2]);
         const float Mu = M == kNegInf ? 0.f : M;
         float a0 = 0.f, a1 = 0.f, sum = 0.f;
 #pragma unroll
-        for (int u = 0; u < kConsumers; ++u) {
-          const float f = tc::ex2(mlbuf[(u * 8 + h) * 2] - Mu);
-          const float2 ov = *reinterpret_cast<const float2*>(obuf + (u * 8 + h) * D + c);
+        for (int u = 0; u < kShare; ++u) {
+          const float f = tc::ex2(mlbuf[((w0 + u) * 8 + h) * 2] - Mu);
+          const float2 ov = *reinterpret_cast<const float2*>(obuf + ((w0 + u) * 8 + h) * D + c);
           a0 = fmaf(f, ov.x, a0);
           a1 = fmaf(f, ov.y, a1);
-          sum = fmaf(f, mlbuf[(u * 8 + h) * 2 + 1], sum);
+          sum = fmaf(f, mlbuf[((w0 + u) * 8 + h) * 2 + 1], sum);
         }
         if (w.whole) {
           const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays NaN
-          const int head = w.g * G + h;
+          const int head = w.g * HP * G + uh;
           T* dst = static_cast<T*>(const_cast<void*>(p.out.data)) + (int64_t)w.b * p.out.sb + (int64_t)head * p.out.sh;
           *reinterpret_cast<uint32_t*>(dst + c) = pack2<T>(a0 * inv, a1 * inv);
           if (p.lse && c == 0)
             p.lse[(int64_t)w.b * p.H + head] = sum == 0.f ? kNegInf : (M + log2f(sum)) / kLog2e;
         } else {
-          *reinterpret_cast<float2*>(p.part_o + (slot * G + h) * D + c) = make_float2(a0, a1);
-          if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * G + h) * 2) = make_float2(M, sum);
+          *reinterpret_cast<float2*>(p.part_o + (slot * HP * G + uh) * D + c) = make_float2(a0, a1);
+          if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * HP * G + uh) * 2) = make_float2(M, sum);
         }
       }
       asm volatile("bar.sync 1, %0;\n" ::"n"(kConsumers * 32) : "memory");
@@ -407,21 +424,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) p.cta_status[blockIdx.x] = *bad;
 }
 
-// One CTA per (KV head, sequence): merges the partials of a divided one in
+// One CTA per (unit's KV heads, sequence): merges the partials of a divided one in
 // order, writes zeros for a sequence without tokens; the first CTA also
 // writes the status word.  Bound by latency: the weights of all parts first (a
 // warp per head), then the outputs, whose loads depend on nothing.
 constexpr int kJoinThreads = 256;
-template <typename T>
+template <typename T, int HP>
 __global__ void __launch_bounds__(kJoinThreads) window_decode_join_kernel(const WindowDecodeParams p) {
-  __shared__ float weight[kMaxDecodeCtas][8];  // of part i for head h, 1 / l included
+  __shared__ float weight[kMaxDecodeCtas][8 * HP];  // of part i for head h of the unit, 1 / l included
   const int g = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.G, D = p.D;
+  const int G = HP * p.G, D = p.D;  // query heads of a unit
   long long total, before;
   batch_steps(p, b, lane, &total, &before);
   const SeqSteps q(p, b);
-  const Cut cut(total * p.Hkv, p.n_cta);
-  const long long u0 = before * p.Hkv + (long long)g * q.n;
+  const Cut cut(total * p.units, p.n_cta);
+  const long long u0 = before * p.units + (long long)g * q.n;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (g == 0 && b == 0 && warp == 0) {
     int code = 0;
@@ -447,20 +464,20 @@ __global__ void __launch_bounds__(kJoinThreads) window_decode_join_kernel(const 
   if (parts == 1) return;  // finished by its CTA
   // part i lies in the second slot of the first CTA, then in the first slot of the others
   auto slot = [&](int i) { return 2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0); };
-  if (warp < G) {
+  for (int h = warp; h < G; h += kJoinThreads / 32) {
     float m = kNegInf, l = 0.f;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[(slot(i) * G + warp) * 2]);
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[(slot(i) * G + h) * 2]);
     const float M = warp_max(m), Mu = M == kNegInf ? 0.f : M;
     for (int i = lane; i < parts; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(i) * G + warp) * 2);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(i) * G + h) * 2);
       const float f = tc::ex2(ml.x - Mu);
-      weight[i][warp] = f;
+      weight[i][h] = f;
       l = fmaf(f, ml.y, l);
     }
     l = warp_sum(l);
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
-    for (int i = lane; i < parts; i += 32) weight[i][warp] *= inv;
-    if (p.lse && lane == 0) p.lse[(int64_t)b * p.H + g * G + warp] = l == 0.f ? kNegInf : (M + log2f(l)) / kLog2e;
+    for (int i = lane; i < parts; i += 32) weight[i][h] *= inv;
+    if (p.lse && lane == 0) p.lse[(int64_t)b * p.H + g * G + h] = l == 0.f ? kNegInf : (M + log2f(l)) / kLog2e;
   }
   __syncthreads();
   for (int e = threadIdx.x * 2; e < G * D; e += kJoinThreads * 2) {
@@ -477,25 +494,26 @@ __global__ void __launch_bounds__(kJoinThreads) window_decode_join_kernel(const 
   }
 }
 
-template <typename T, int D>
-cudaError_t run(const WindowDecodeParams& p, cudaStream_t stream) {
-  using L = Layout<D>;
+template <typename T, int D, int HP>
+cudaError_t run(WindowDecodeParams p, cudaStream_t stream) {
+  using L = Layout<D, HP>;
+  p.units = p.Hkv / HP;
   CUtensorMap mk, mv;
   const int64_t rows = p.block_table ? p.block : p.Lmax, outer = p.block_table ? p.n_pages : p.B;
-  // D = 64: a token's 128 bytes of one KV head.  With 256-byte fetches the
-  // next head's came too and were gone again before their turn: 705 MB read
-  // for 537 (16 sequences of up to 16K tokens, 16 KV heads).
-  if (!make_map(&mk, p.k, p.dtype, outer, rows, p.Hkv, D, 1, kStep, D == 64) ||
-      !make_map(&mv, p.v, p.dtype, outer, rows, p.Hkv, D, 1, kStep, D == 64))
+  // a single 64-wide head: with 256-byte L2 fetches the next head's 128 bytes
+  // came too and were gone again before their turn (705 MB read for 537)
+  const bool narrow = D == 64 && HP == 1;
+  if (!make_map(&mk, p.k, p.dtype, outer, rows, p.Hkv, D, 1, kStep, narrow) ||
+      !make_map(&mv, p.v, p.dtype, outer, rows, p.Hkv, D, 1, kStep, narrow))
     return cudaErrorInvalidValue;
-  auto kern = window_decode_kernel<T, D>;
+  auto kern = window_decode_kernel<T, D, HP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   kern<<<p.n_cta, kThreads, L::kAlloc, stream>>>(mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the join's launch overlaps the streaming kernel's end; it waits for its results itself
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.Hkv, p.B);
+  cfg.gridDim = dim3(p.units, p.B);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -503,15 +521,21 @@ cudaError_t run(const WindowDecodeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, window_decode_join_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, window_decode_join_kernel<T, HP>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream) {
   if (p.D == 128)
-    return p.dtype == 1 ? run<__half, 128>(p, stream) : run<__nv_bfloat16, 128>(p, stream);
-  return p.dtype == 1 ? run<__half, 64>(p, stream) : run<__nv_bfloat16, 64>(p, stream);
+    return p.dtype == 1 ? run<__half, 128, 1>(p, stream) : run<__nv_bfloat16, 128, 1>(p, stream);
+  // pairs of heads when the visible tokens, if the sequences are as long as
+  // they may be, give every CTA two steps of pairs (lengths are the device's)
+  const int64_t seen = p.window > 0 ? std::min<int64_t>(p.Lmax, (int64_t)p.window + p.sinks) : p.Lmax;
+  const int64_t steps = (seen + kStep - 1) / kStep * p.B * (p.Hkv / 2);
+  if (p.Hkv % 2 == 0 && steps >= kMinUnits * (int64_t)p.n_cta)
+    return p.dtype == 1 ? run<__half, 64, 2>(p, stream) : run<__nv_bfloat16, 64, 2>(p, stream);
+  return p.dtype == 1 ? run<__half, 64, 1>(p, stream) : run<__nv_bfloat16, 64, 1>(p, stream);
 }
 
 }  // namespace dash

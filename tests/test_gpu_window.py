@@ -314,6 +314,9 @@ DECODE = {
     "window_sinks128": (8, 8, 128, F16, 64, 128, [64, 128, 191, 192, 193, 256, 3000]),
     "window_g1": (2, 2, 128, BF16, 300, 7, [5000, 301, 308, 10]),
     "sinks_in_band": (4, 2, 64, F16, 130, 100, [140, 230, 231, 300]),
+    "pairs": (4, 4, 64, F16, 0, 0, [3000, 0, 1, 777, 64, 2999, 128, 500]),  # 64-wide KV heads two at a time
+    "pairs_g8_window": (16, 2, 64, BF16, 500, 70, [(97 * i) % 1500 for i in range(40)]),
+    "pairs_odd_heads": (6, 3, 64, F16, 0, 0, [2500, 100, 1900, 2000]),
     "many": (2, 1, 64, F16, 0, 0, [(37 * i) % 300 for i in range(200)]),
 }
 
