@@ -492,6 +492,7 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
  *   lse        device fp32 [B, H] or NULL.
  *   workspace  dash_attn_window_decode_workspace_size() bytes, 256-byte
  *              aligned; it depends on the current device, not on B or Lmax.
+ *              Calls that may run at the same time need one each.
  * Cache values at tokens that are not visible are never used.  The result
  * does not depend on timing.  The call can be captured into a graph; the work
  * is split on the device by the lengths that seqlens holds when it runs.
@@ -518,11 +519,15 @@ dash_status_t dash_attn_window_decode_paged(const dash_tensor_t* q, const dash_t
  * One table serves the pools of all layers.  The calls only touch this state;
  * dash_attn_pages_copy moves the pages' contents.  New pages are the lowest
  * free ones, so every call is a function of the state.  Each call is one
- * launch and can be captured into a graph.  What the state does not allow (a
- * sequence out of range, the same destination twice, a length out of range)
- * is found on the device before the first write: the call changes nothing
- * and the workspace status word reads DASH_ERR_INVALID_ARGUMENT.  block is
- * 64 or 128; at most 8192 sequences, batch * max_blocks and n_pages below 2^30.
+ * launch and can be captured into a graph.  What fork, free and grow do not
+ * allow (a sequence out of range, the same destination twice, a length out of
+ * range, in grow a shared last page outside the pool) is found on the device
+ * before the first write: the call changes nothing and the workspace status
+ * word reads DASH_ERR_INVALID_ARGUMENT.  A held table entry outside the pool
+ * is never followed: fork and free move it without counting it, compact
+ * leaves it as it is, and the status word reads DASH_ERR_INVALID_ARGUMENT.
+ * block is 64 or 128; at most 8192 sequences, batch * max_blocks and n_pages
+ * at most 2^30.  table, seqlens, refs and the lists are separate arrays.
  *   workspace  dash_attn_pages_workspace_size() bytes, 256-byte aligned.
  */
 size_t dash_attn_pages_workspace_size(int64_t batch, int64_t max_blocks, int64_t n_pages);

@@ -755,7 +755,8 @@ def window_fwd(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor |
         ws, room = _scratch(_lib.dash_attn_window_fwd_workspace_size(qd, kd), "dash_attn_window_fwd_workspace_size",
                             q.device, workspace)
         _check(_lib.dash_attn_window_fwd(qd, kd, _packed(v), _array(seqlens, "seqlens", (B,)), window, sinks,
-                                         _packed(out), _array(lse, "lse", (B, H, S), torch.float32), ws.data_ptr(), room, s))
+                                         _packed(out), _array(lse, "lse", (B, H, S), torch.float32), ws.data_ptr(),
+                                         room, s))
     return (out, lse) if return_lse else out
 
 
@@ -870,8 +871,8 @@ def pages_fork(block_table, seqlens, refs, src, dst, block: int, workspace=None,
         state = _pages_state(block_table, seqlens, refs)
         n = dst.numel()
         ws, room = _pages_scratch(state, block_table.device, workspace)
-        _check(_lib.dash_attn_pages_fork(*state, _array(src, "src", (n,)), _array(dst, "dst", (n,)), n, block, ws.data_ptr(),
-                                         room, s))
+        _check(_lib.dash_attn_pages_fork(*state, _array(src, "src", (n,)), _array(dst, "dst", (n,)), n, block,
+                                         ws.data_ptr(), room, s))
 
 
 def pages_free(block_table, seqlens, refs, slots, block: int, workspace=None, stream=None) -> None:

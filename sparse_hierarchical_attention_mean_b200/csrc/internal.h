@@ -171,11 +171,9 @@ struct PairParams {
 };
 cudaError_t launch_pairs(const PairParams& p, cudaStream_t stream);
 // 4-D TMA map over a [B, S, H, D] f16/bf16 view (innermost first: D, H, S,
-// B), 128-byte swizzle, box {64, box_h, box_s, 1}; no multicast.  narrow: L2
-// fetches 128 bytes at a time instead of 256 (for one head's 128-byte rows
-// among others' that are not wanted soon).
+// B), 128-byte swizzle, box {64, box_h, box_s, 1}; no multicast.
 bool make_map(CUtensorMap* map, const View& v, int dtype, int64_t B, int64_t S, int64_t H, int D, int box_h,
-              int box_s, bool narrow = false);
+              int box_s);
 cudaError_t launch_sparse_prefill(const SparseParams& p, cudaStream_t stream);
 cudaError_t launch_sparse_prefill_tc(const SparseParams& p, cudaStream_t stream);
 

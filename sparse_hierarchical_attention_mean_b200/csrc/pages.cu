@@ -351,7 +351,8 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
 constexpr int kCopyChunk = kCopyThreads * kCopyUnroll * 16;
 
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PageCopyParams p, int chunks) {
+__global__ void __launch_bounds__(kCopyThreads)
+    pages_copy_kernel(const __grid_constant__ PageCopyParams p, int chunks) {
   const int64_t entry = blockIdx.x / chunks;
   const int chunk = blockIdx.x % chunks;
   const PagePool& pool = p.pool[blockIdx.y];

@@ -219,17 +219,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Registers per thread of the calling warpgroup (all four warps call it); the
-// block's sum must stay within what it was launched with.
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-
 // ------------------------------------------------------------------ descriptors
 
 // Shared-memory matrix descriptor (tcgen05): start address, leading and

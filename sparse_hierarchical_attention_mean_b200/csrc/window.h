@@ -68,6 +68,14 @@ __device__ __forceinline__ void begin_status(const WindowParams& p, int lane) {
   }
 }
 
+// 4-D TMA map over a [B, S, H, D] f16/bf16 view (innermost first: D, H, S, B),
+// 128-byte swizzle, box {64, box_h, box_s, 1}; no multicast.  Strides must be
+// valid for every extent (solid views).  narrow: L2 fetches 128 bytes at a
+// time instead of 256 (for one head's 128-byte rows among others' that are not
+// wanted soon).
+bool window_map(CUtensorMap* map, const View& v, int dtype, int64_t B, int64_t S, int64_t H, int D, int box_h,
+                int box_s, bool narrow = false);
+
 // f16 / bf16 tensor-core path
 cudaError_t launch_window_fwd_tc(const WindowParams& p, cudaStream_t stream);
 cudaError_t launch_window_bwd_tc(const WindowParams& p, cudaStream_t stream);

@@ -858,8 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (w.slot >= 0) {
           // [b, g][slot][dk, dv][128][D] fp32
-          float* dst = p.part + ((((int64_t)(w.b * p.Hkv + w.g) * (p.n_chunks + 1) + w.slot) * 2 + is_v) * kRows + k) * D +
-                       col;
+          const int64_t slot = (int64_t)(w.b * p.Hkv + w.g) * (p.n_chunks + 1) + w.slot;
+          float* dst = p.part + ((slot * 2 + is_v) * kRows + k) * D + col;
 #pragma unroll
           for (int e = 0; e < 64; e += 4)
             *reinterpret_cast<uint4*>(dst + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -944,11 +944,11 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
   if (std::max(row_items, key_items) > 0x7fffffff - 4096) return cudaErrorInvalidValue;
   cudaError_t e;
   CUtensorMap mq, mdo, mo, mk, mv;
-  if (!make_map(&mq, p.q, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
-      !make_map(&mdo, p.dout, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
-      !make_map(&mo, p.out, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
-      !make_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows) ||
-      !make_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows))
+  if (!window_map(&mq, p.q, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
+      !window_map(&mdo, p.dout, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
+      !window_map(&mo, p.out, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
+      !window_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows) ||
+      !window_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows))
     return cudaErrorInvalidValue;
   {
     using L = RowLayout<D>;
@@ -963,9 +963,10 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
     auto kern = window_bwd_key_tc_kernel<T, D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
-    if ((e = launch_early(kern, dim3((unsigned)std::min<int64_t>(key_items, p.num_sms)), kThreads, L::kAlloc, stream, mq,
-                          mdo, mk, mv, p, (p.S + kRows - 1) / kRows + p.n_chunks)) != cudaSuccess)
-      return e;
+    const dim3 grid((unsigned)std::min<int64_t>(key_items, p.num_sms));
+    const int per_head = (p.S + kRows - 1) / kRows + p.n_chunks;
+    e = launch_early(kern, grid, kThreads, L::kAlloc, stream, mq, mdo, mk, mv, p, per_head);
+    if (e != cudaSuccess) return e;
   }
   if (p.n_chunks > 0)
     e = launch_early(window_bwd_join_kernel<T, D>, dim3(p.B * p.Hkv, 2 * kRows * D / 1024), 256, 0, stream, p);

@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A fragments of the query heads (rows gq >= G and 8..15 are zero)
       uint32_t qa[KS][2];
       {
-        const T* src = static_cast<const T*>(p.q.data) + (int64_t)w.b * p.q.sb + (int64_t)((w.g * HP + hs) * G + gq) * p.q.sh;
+        const T* src = static_cast<const T*>(p.q.data) + (int64_t)w.b * p.q.sb +
+                       (int64_t)((w.g * HP + hs) * G + gq) * p.q.sh;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
           qa[kk][0] = gq < G ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * tq) : 0u;
@@ -503,8 +504,8 @@ cudaError_t run(WindowDecodeParams p, cudaStream_t stream) {
   // a single 64-wide head: with 256-byte L2 fetches the next head's 128 bytes
   // came too and were gone again before their turn (705 MB read for 537)
   const bool narrow = D == 64 && HP == 1;
-  if (!make_map(&mk, p.k, p.dtype, outer, rows, p.Hkv, D, 1, kStep, narrow) ||
-      !make_map(&mv, p.v, p.dtype, outer, rows, p.Hkv, D, 1, kStep, narrow))
+  if (!window_map(&mk, p.k, p.dtype, outer, rows, p.Hkv, D, 1, kStep, narrow) ||
+      !window_map(&mv, p.v, p.dtype, outer, rows, p.Hkv, D, 1, kStep, narrow))
     return cudaErrorInvalidValue;
   auto kern = window_decode_kernel<T, D, HP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp >= 4 * kTiles) {
-    tc::reg_dec<kOtherRegs>();
+    reg_dec<kOtherRegs>();
     if (warp == kProducerWarp) {
       // ------------------------------------------------------------ producer
       if (blockIdx.x == 0) begin_status(p, lane);
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    tc::reg_inc<kSoftmaxRegs>();
+    reg_inc<kSoftmaxRegs>();
     const int t = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
     const uint32_t tb = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t tb_o = tb + kColO + t * 128;
@@ -412,9 +412,9 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
   using L = Layout<D>;
   CUtensorMap mq, mk, mv;
   const int P = kRows / p.G;
-  if (!make_map(&mq, p.q, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
-      !make_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kStep) ||
-      !make_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kStep))
+  if (!window_map(&mq, p.q, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
+      !window_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kStep) ||
+      !window_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kStep))
     return cudaErrorInvalidValue;
   auto kern = window_fwd_tc_kernel<T, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);

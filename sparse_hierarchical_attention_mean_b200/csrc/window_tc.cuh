@@ -9,6 +9,17 @@
 
 namespace dash {
 
+// Registers per thread of the calling warpgroup (all four warps call it); the
+// block's sum must stay within what it was launched with.
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 // Waits for phase `phase` of a barrier (counted from 0); the answer is the
 // same for the whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase) {
