@@ -442,6 +442,7 @@ dash_status_t dash_attn_sparse_mask(const dash_tensor_t* q, const dash_tensor_t*
  *            logits; NULL in the forward if not wanted.  The backward reads
  *            the forward's.
  * Strides of 0 over an extent above 1 are refused (DASH_ERR_UNSUPPORTED).
+ * Outputs must not overlap inputs.
  */
 
 /* Bytes of workspace of dash_attn_window_fwd (a status word). 0: rejected arguments. */
@@ -463,7 +464,9 @@ dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* 
  *   dS_ij = p_ij (dout_i . v_j - dout_i . out_i);  dq_i = sum_j dS_ij k_j / sqrt(d);
  *   dk_j = sum_i dS_ij q_i / sqrt(d);  dv_j = sum_i p_ij dout_i
  * (dk and dv summed over the heads of the group).  No atomics: the same
- * result every time.
+ * result every time.  f16/bf16: p and dS are rounded to the input type for the
+ * products (f16: a dS beyond 65504 overflows); D = dout . out is taken from
+ * the out given.
  *   out, lse   the forward's, with the same q, k, v, seqlens, window, sinks.
  *   workspace  dash_attn_window_bwd_workspace_size() bytes, 256-byte aligned.
  */
@@ -579,8 +582,8 @@ dash_status_t dash_attn_pages_compact(const int32_t* block_table, int64_t batch,
  * Page src[i] of every pool to page dst[i] (i < n, device int32).  Entries
  * below 0 or outside the pool are skipped.  No dst may be a src or a dst of
  * another entry (the lists of dash_attn_pages_grow and _compact are so).
- *   pools  n_pools host descriptors [n_pages, s, h, d] of one shape beyond
- *          the first dimension, and one dtype (K and V of every layer; the
+ *   pools  n_pools (1 .. 64) host descriptors [n_pages, s, h, d] of one shape
+ *          beyond the first dimension (n_pages up to 2^30), and one dtype (K and V of every layer; the
  *          summaries [B, Hkv, t_cap, d] of sparse layers are a pool whose
  *          pages are the sequences).
  */

@@ -795,7 +795,10 @@ class _WindowAttention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, seqlens = ctx.saved_tensors
-        g = window_bwd(q, k, v, out, lse, dout.contiguous(), *ctx.args, seqlens)
+        dout = dout.contiguous()
+        if dout.data_ptr() % 16:  # a view that starts between two 16-byte pieces
+            dout = dout.clone()
+        g = window_bwd(q, k, v, out, lse, dout, *ctx.args, seqlens)
         return g["dq"], g["dk"], g["dv"], None, None, None
 
 

@@ -1330,9 +1330,18 @@ dash::View solid_view(const dash_tensor_t* t) {
   return v;
 }
 
-dash_status_t check_solid(const dash_tensor_t* t, const char* name) {
+// pool: pages, of which there may be more than sequences.
+dash_status_t check_solid(const dash_tensor_t* t, const char* name, bool pool = false) {
   dash_status_t st;
-  if ((st = check_tensor(t, name))) return st;
+  if (pool && t && t->b > 0) {
+    if (t->b > (1LL << 30)) return fail(DASH_ERR_UNSUPPORTED, "%s: more than 2^30 pages", name);
+    dash_tensor_t page = *t;
+    page.b = 1;
+    st = check_tensor(&page, name);
+  } else {
+    st = check_tensor(t, name);
+  }
+  if (st) return st;
   if ((t->b > 1 && t->stride_b == 0) || (t->s > 1 && t->stride_s == 0) || (t->h > 1 && t->stride_h == 0))
     return fail(DASH_ERR_UNSUPPORTED, "%s: a stride of 0 over an extent above 1", name);
   return DASH_OK;
@@ -1353,10 +1362,10 @@ dash_status_t check_workspace(const void* workspace, size_t bytes, size_t need) 
   return DASH_OK;
 }
 
-dash_status_t check_like(const dash_tensor_t* t, const dash_tensor_t* like, const char* name) {
+dash_status_t check_like(const dash_tensor_t* t, const dash_tensor_t* like, const char* name, bool pool = false) {
   dash_status_t st;
-  if ((st = check_solid(t, name))) return st;
-  if (t->dtype != like->dtype) return fail(DASH_ERR_INVALID_ARGUMENT, "%s: dtype differs from q's", name);
+  if ((st = check_solid(t, name, pool))) return st;
+  if (t->dtype != like->dtype) return fail(DASH_ERR_INVALID_ARGUMENT, "%s: dtype differs from its counterpart's", name);
   if (t->b != like->b || t->s != like->s || t->h != like->h || t->d != like->d)
     return fail(DASH_ERR_INVALID_ARGUMENT, "%s: shape mismatch", name);
   return DASH_OK;
@@ -1518,8 +1527,8 @@ dash_status_t run_window_decode(const dash_tensor_t* q, const dash_tensor_t* k, 
                                 int64_t window, int64_t sinks, dash_tensor_t* out, float* lse, void* workspace,
                                 size_t workspace_bytes, dash_stream_t stream) {
   dash_status_t st;
-  if ((st = check_solid(q, "q")) || (st = check_solid(k, table ? "k_pages" : "kcache")) ||
-      (st = check_like(v, k, table ? "v_pages" : "vcache")) || (st = check_like(out, q, "out")) ||
+  if ((st = check_solid(q, "q")) || (st = check_solid(k, table ? "k_pages" : "kcache", table)) ||
+      (st = check_like(v, k, table ? "v_pages" : "vcache", table)) || (st = check_like(out, q, "out")) ||
       (st = check_group(q->h, k->h)) || (st = check_window(window, sinks)))
     return st;
   if (q->s != 1) return fail(DASH_ERR_INVALID_ARGUMENT, "decode takes one query token (s == 1)");
@@ -1581,7 +1590,7 @@ dash_status_t dash_attn_window_decode_paged(const dash_tensor_t* q, const dash_t
                                             dash_tensor_t* out, float* lse, void* workspace, size_t workspace_bytes,
                                             dash_stream_t stream) {
   dash_status_t st;
-  if ((st = check_tensor(k_pages, "k_pages"))) return st;
+  if ((st = check_solid(k_pages, "k_pages", true))) return st;
   if (k_pages->s != 64 && k_pages->s != 128)
     return fail(DASH_ERR_UNSUPPORTED, "page size %lld not in {64, 128}", (long long)k_pages->s);
   if (!block_table || max_blocks < 1)
@@ -1732,7 +1741,7 @@ dash_status_t dash_attn_pages_copy(const dash_tensor_t* pools, int64_t n_pools, 
   for (int64_t i = 0; i < n_pools; ++i) {
     const dash_tensor_t& t = pools[i];
     dash_status_t st;
-    if ((st = check_solid(&t, "pool"))) return st;
+    if ((st = check_solid(&t, "pool", true))) return st;
     if (t.dtype != first.dtype || t.s != first.s || t.h != first.h || t.d != first.d)
       return fail(DASH_ERR_INVALID_ARGUMENT, "pools of different dtypes or page shapes");
     const dash::View v = solid_view(&t);

@@ -178,6 +178,11 @@ def test_autograd(cuda_lib, dtype):
     assert torch.equal(out.detach(), plain)
     for t, n in zip(leaves, ("dq", "dk", "dv")):
         assert torch.equal(t.grad, want[n])
+    # an incoming gradient that does not start at a 16-byte boundary
+    odd = torch.cat([do.flatten()[:1], do.flatten()])[1:].view(do.shape)
+    assert odd.data_ptr() % 16 != 0
+    (gk,) = torch.autograd.grad(dash.window_attention(q, k, v, 40, 3, seqlens), k, odd)
+    assert torch.equal(gk, want["dk"])
     total = dash.window_attention(q, k, v, 40, 3, seqlens).sum()
     (gq,) = torch.autograd.grad(total, q)
     ones = dash.window_bwd(q.detach(), k.detach(), v.detach(), plain, lse, torch.ones_like(do), 40, 3, seqlens)["dq"]
@@ -429,6 +434,47 @@ def test_decode_offsets_past_32_bits(cuda_lib):
     lens = torch.tensor([250, 250], dtype=torch.int32, device="cuda")
     both = dash.window_decode(q.expand(2, 1, 8, d).contiguous(), far, far, lens)
     assert torch.equal(both[0], both[1]) and torch.equal(both[:1], got)
+
+
+def test_more_pages_than_sequences_may_be(cuda_lib):
+    """Pools of more than 65535 pages."""
+    dash = cuda_lib
+    n_pages = 70000
+    pool = torch.zeros(n_pages, 64, 1, 64, dtype=F16, device="cuda")
+    ids = [69999, 66000, 5]
+    pool[ids] = torch.randn(3, 64, 1, 64, device="cuda").half()
+    dash.pages_copy([pool], torch.tensor([69999, 5], dtype=torch.int32, device="cuda"),
+                    torch.tensor([7, 69998], dtype=torch.int32, device="cuda"))
+    assert torch.equal(pool[7], pool[69999]) and torch.equal(pool[69998], pool[5])
+    q = torch.randn(1, 1, 2, 64, device="cuda").half()
+    table = torch.tensor([[69999, 66000, 69998]], dtype=torch.int32, device="cuda")
+    seqlens = torch.tensor([190], dtype=torch.int32, device="cuda")
+    got, lse = dash.window_decode_paged(q, pool, pool, table, seqlens, return_lse=True)
+    cache = pool[ids].reshape(1, 192, 1, 64)
+    _check_decode((2, 1, 64, F16, 0, 0, [190]), q, cache, cache, got, lse)
+
+
+def test_calls_on_two_streams_at_once(cuda_lib):
+    """Calls that overlap, each with its own buffers, give what they give alone."""
+    dash = cuda_lib
+    case = (1, 3000, 8, 2, 128, BF16, 500, 20, None)
+    one, two = _inputs(case, 11), _inputs(case, 12)
+    dec = _decode_inputs(DECODE["pairs"], 5)
+
+    def work(x, stream):
+        q, k, v, do, _ = x
+        out, lse = dash.window_fwd(q, k, v, 500, 20, return_lse=True, stream=stream)
+        g = dash.window_bwd(q, k, v, out, lse, do, 500, 20, stream=stream)
+        return [out, lse, g["dq"], g["dk"], g["dv"], dash.window_decode(*dec, stream=stream)]
+
+    want = [work(x, None) for x in (one, two)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[work(x, s) for x, s in zip((one, two), streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for round_ in got:
+        for a, b in zip(round_, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_decode_captured_with_growing_lengths(cuda_lib):
