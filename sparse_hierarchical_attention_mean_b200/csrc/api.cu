@@ -1347,6 +1347,12 @@ dash_status_t check_solid(const dash_tensor_t* t, const char* name, bool pool = 
   return DASH_OK;
 }
 
+// Rows of a 16-bit output start at multiples of 32 bytes.
+bool wide_rows(const dash_tensor_t* t) {
+  const dash::View v = solid_view(t);
+  return (reinterpret_cast<uintptr_t>(t->data) | (v.sb | v.ss | v.sh) * 2) % 32 == 0;
+}
+
 dash_status_t check_window(int64_t window, int64_t sinks) {
   if (window < 0) return fail(DASH_ERR_INVALID_ARGUMENT, "window %lld < 0", (long long)window);
   if (sinks < 0) return fail(DASH_ERR_INVALID_ARGUMENT, "sinks %lld < 0", (long long)sinks);
@@ -1460,6 +1466,7 @@ dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* 
   if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
   cudaStream_t s = (cudaStream_t)stream;
   dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, lse);
+  p.wide = wide_rows(out);
   p.status = at<dash::DeviceStatus>(workspace, L.status);
   const cudaError_t e = q->dtype == DASH_F32 ? dash::launch_window_fwd_simt(p, s) : dash::launch_window_fwd_tc(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "window forward");
@@ -1491,6 +1498,7 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
   p.dq = solid_view(dq);
   p.dk = solid_view(dk);
   p.dv = solid_view(dv);
+  p.wide = wide_rows(dq) && wide_rows(dk) && wide_rows(dv);
   p.dd = at<float>(workspace, L.dd);
   p.ndd = p.dd;
   p.nlse2 = at<float>(workspace, L.nlse2);

@@ -32,6 +32,7 @@ struct WindowParams {
   int n_chunks;             // items of chunk_tiles row tiles that see only sinks of the first 128 keys
   int chunk_tiles;
   int num_sms;
+  bool wide;                // rows of every output start at multiples of 32 bytes
   DeviceStatus* status;
 };
 

@@ -444,28 +444,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || !(ok = warp_wait(&bars->dq_full, item))) break;
       tc::fence_after_sync();
       if (more) rows_to_tmem();
-      // ---- dq of the item, 64 columns a warp (half 0 all of them at D = 64)
-      if (half < L::KC) {
-        const bool live = pos < w.n;
-        uint4 row[8];
+      // ---- dq of the item, each half of the workers takes half of the columns
+      const bool live = pos < w.n;
+      T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb +
+               (int64_t)min(pos, p.S - 1) * p.dq.ss + (int64_t)(w.g * p.G + (r & (p.G - 1))) * p.dq.sh;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[32];
-          tc::tmem_ld32(tb + kColDQ + half * 64 + c * 32, v);
-          tc::tmem_wait_ld();
+      for (int c = 0; c < D / 64; ++c) {
+        const int col = (half * (D / 64) + c) * 32;
+        uint32_t v[32];
+        tc::tmem_ld32(tb + kColDQ + col, v);
+        tc::tmem_wait_ld();
+        if (!live) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            row[c * 4 + e] = live ? pack8<T>(v + e * 8, rsqrtf((float)D)) : make_uint4(0u, 0u, 0u, 0u);
+          for (int j = 0; j < 32; ++j) v[j] = 0u;
         }
-        transpose8(row, lane);
-        T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb + half * 64 + (lane & 7) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rr = q4 * 32 + (lane & 24) + e, pp = w.pos0 + (rr >> lg);
-          if (pp < p.S)
-            *reinterpret_cast<uint4*>(dst + (int64_t)pp * p.dq.ss +
-                                      (int64_t)(w.g * p.G + (rr & (p.G - 1))) * p.dq.sh) = row[e];
-        }
+        if (pos < p.S) store_row32(dst + col, v, rsqrtf((float)D), p.wide);
       }
       tc::fence_before_sync();
       warp_arrive(&bars->dq_empty, lane);
@@ -839,42 +832,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float ksc = rsqrtf((float)D);
       const bool live = key < w.n;
-      // 64 columns of dk and of dv a warp (D = 64: dk in half 0, dv in half 1)
+      // each half of the workers takes half of the columns
 #pragma unroll 1
       for (int o = 0; o < 2; ++o) {
-        const bool is_v = D == 64 ? half : o;
-        if (D == 64 && o > 0) break;
-        const int col = D == 64 ? 0 : half * 64;
-        uint32_t v[64];
-        if (any) {
-          const uint32_t src = tb + (is_v ? kColDV : kColDK) + col;
-          tc::tmem_ld32(src, v);
-          tc::tmem_ld32(src + 32, v + 32);
-          tc::tmem_wait_ld();
-        }
-        if (!any || !live) {
+        const View& out = o ? p.dv : p.dk;
+        T* dst = static_cast<T*>(const_cast<void*>(out.data)) + (int64_t)w.b * out.sb +
+                 (int64_t)min(key, p.S - 1) * out.ss + (int64_t)w.g * out.sh;
+        // [b, g][slot][dk, dv][128][D] fp32
+        const int64_t slot = (int64_t)(w.b * p.Hkv + w.g) * (p.n_chunks + 1) + w.slot;
+        float* part = p.part + ((slot * 2 + o) * kRows + k) * D;
 #pragma unroll
-          for (int j = 0; j < 64; ++j) v[j] = 0u;
-        }
-        if (w.slot >= 0) {
-          // [b, g][slot][dk, dv][128][D] fp32
-          const int64_t slot = (int64_t)(w.b * p.Hkv + w.g) * (p.n_chunks + 1) + w.slot;
-          float* dst = p.part + ((slot * 2 + is_v) * kRows + k) * D + col;
+        for (int c = 0; c < D / 64; ++c) {
+          const int col = (half * (D / 64) + c) * 32;
+          uint32_t v[32];
+          if (any) {
+            tc::tmem_ld32(tb + (o ? kColDV : kColDK) + col, v);
+            tc::tmem_wait_ld();
+          }
+          if (!any || !live) {
 #pragma unroll
-          for (int e = 0; e < 64; e += 4)
-            *reinterpret_cast<uint4*>(dst + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        } else {
-          uint4 row[8];
+            for (int j = 0; j < 32; ++j) v[j] = 0u;
+          }
+          if (w.slot >= 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) row[e] = pack8<T>(v + e * 8, is_v ? 1.f : ksc);
-          transpose8(row, lane);
-          const View& out = is_v ? p.dv : p.dk;
-          T* dst = static_cast<T*>(const_cast<void*>(out.data)) + (int64_t)w.b * out.sb + (int64_t)w.g * out.sh + col +
-                   (lane & 7) * 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int kk = w.k0 + q4 * 32 + (lane & 24) + e;
-            if (kk < p.S) *reinterpret_cast<uint4*>(dst + (int64_t)kk * out.ss) = row[e];
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + col + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          } else if (key < p.S) {
+            store_row32(dst + col, v, o ? 1.f : ksc, p.wide);
           }
         }
       }

@@ -366,28 +366,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(&bars->o_full[t], items))) break;
         tc::fence_after_sync();
       }
-#pragma unroll 1
-      for (int cc = 0; cc < L::KC; ++cc) {
-        uint4 row[8];
+      T* dst = static_cast<T*>(const_cast<void*>(p.out.data)) + (int64_t)w.b * p.out.sb +
+               (int64_t)min(pos, p.S - 1) * p.out.ss + (int64_t)head * p.out.sh;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t ov[32];
-          if (w.steps > 0) {
-            tc::tmem_ld32(tb_o + cc * 64 + c * 32, ov);
-            tc::tmem_wait_ld();
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) row[c * 4 + e] = live ? pack8<T>(ov + e * 8, inv) : make_uint4(0u, 0u, 0u, 0u);
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t ov[32];
+        if (w.steps > 0) {
+          tc::tmem_ld32(tb_o + cc * 32, ov);
+          tc::tmem_wait_ld();
         }
-        transpose8(row, lane);
-        T* dst = static_cast<T*>(const_cast<void*>(p.out.data)) + (int64_t)w.b * p.out.sb + cc * 64 + (lane & 7) * 8;
+        if (!live) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int rr = q4 * 32 + (lane & 24) + x, pp = pos_a + (rr >> lg);
-          if (pp < p.S)
-            *reinterpret_cast<uint4*>(dst + (int64_t)pp * p.out.ss +
-                                      (int64_t)(w.g * p.G + (rr & (p.G - 1))) * p.out.sh) = row[x];
+          for (int j = 0; j < 32; ++j) ov[j] = 0u;
         }
+        if (pos < p.S) store_row32(dst + cc * 32, ov, inv, p.wide);
       }
       if (w.steps > 0) {
         tc::fence_before_sync();
