@@ -452,11 +452,15 @@ size_t dash_attn_window_fwd_workspace_size(const dash_tensor_t* q, const dash_te
  * Forward over q [B, S, H, d], k, v [B, S, Hkv, d] -> out [B, S, H, d], every
  * element written.  f16/bf16: tensor cores, P rounded to the input type for
  * the second product; f32: CUDA cores throughout.
+ *   rest       NULL, or (f16 / bf16) a tensor like out for what rounding took
+ *              from it: out + rest is the output to about twice the bits.  The
+ *              backward's dq is the better for it where few keys are visible.
  *   workspace  dash_attn_window_fwd_workspace_size() bytes, 256-byte aligned.
  */
 dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
                                    const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* out,
-                                   float* lse, void* workspace, size_t workspace_bytes, dash_stream_t stream);
+                                   dash_tensor_t* rest, float* lse, void* workspace, size_t workspace_bytes,
+                                   dash_stream_t stream);
 
 /*
  * Backward: the gradients of sum(dout * out) with respect to q, k and v, in
@@ -465,18 +469,19 @@ dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* 
  *   dk_j = sum_i dS_ij q_i / sqrt(d);  dv_j = sum_i p_ij dout_i
  * (dk and dv summed over the heads of the group).  No atomics: the same
  * result every time.  f16/bf16: p and dS are rounded to the input type for the
- * products (f16: a dS beyond 65504 overflows); D = dout . out is taken from
- * the out given.
- *   out, lse   the forward's, with the same q, k, v, seqlens, window, sinks.
+ * products (dS in dq's to twice its bits where window + sinks <= 16; f16: a dS
+ * beyond 65504 overflows).
+ *   out, rest, lse  the forward's, with the same q, k, v, seqlens, window,
+ *              sinks; rest may be NULL.
  *   workspace  dash_attn_window_bwd_workspace_size() bytes, 256-byte aligned.
  */
 size_t dash_attn_window_bwd_workspace_size(const dash_tensor_t* q, const dash_tensor_t* k, int64_t window,
                                            int64_t sinks);
 dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
-                                   const dash_tensor_t* out, const float* lse, const dash_tensor_t* dout,
-                                   const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* dq,
-                                   dash_tensor_t* dk, dash_tensor_t* dv, void* workspace, size_t workspace_bytes,
-                                   dash_stream_t stream);
+                                   const dash_tensor_t* out, const dash_tensor_t* rest, const float* lse,
+                                   const dash_tensor_t* dout, const int32_t* seqlens, int64_t window, int64_t sinks,
+                                   dash_tensor_t* dq, dash_tensor_t* dk, dash_tensor_t* dv, void* workspace,
+                                   size_t workspace_bytes, dash_stream_t stream);
 
 /*
  * The same attention for one new token per sequence over its cache: the

@@ -154,9 +154,9 @@ def _load() -> ctypes.CDLL:
         "dash_attn_bwd": (i32, [T, T, T, vp, T, T, f32, i32, i32, O, T, T, T, vp, vp, sz, vp]),
         # tensor descriptors as plain pointers: the binding passes them packed (_packed)
         "dash_attn_window_fwd_workspace_size": (sz, [vp, vp]),
-        "dash_attn_window_fwd": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+        "dash_attn_window_fwd": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]),
         "dash_attn_window_bwd_workspace_size": (sz, [vp, vp, i64, i64]),
-        "dash_attn_window_bwd": (i32, [vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]),
+        "dash_attn_window_bwd": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]),
         "dash_attn_window_decode_workspace_size": (sz, [i64, i64, i64]),
         "dash_attn_window_decode": (i32, [vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
         "dash_attn_window_decode_paged": (i32, [vp, vp, vp, vp, i64, vp, i64, i64, vp, vp, vp, sz, vp]),
@@ -740,13 +740,14 @@ def window_fwd_workspace_size(q: torch.Tensor, k: torch.Tensor) -> int:
 
 
 def window_fwd(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None, out=None,
-               return_lse: bool = False, lse=None, workspace=None, stream=None):
+               return_lse: bool = False, lse=None, rest=None, workspace=None, stream=None):
     """Causal attention over a sliding window and the first ``sinks`` tokens (see dash_attn_window_fwd).
 
     window 0: every earlier token.  seqlens: optional int32 [B], the valid tokens of each sequence of a padded
-    batch.  Returns out [B, S, H, d], and with ``return_lse`` the log-sum-exp [B, H, S] fp32 too.
+    batch.  rest: optional tensor like out (f16 / bf16) that receives what rounding took from it.  Returns out
+    [B, S, H, d], and with ``return_lse`` the log-sum-exp [B, H, S] fp32 too.
     """
-    with _On(stream, q, k, v, seqlens, out, lse, workspace) as s:
+    with _On(stream, q, k, v, seqlens, out, lse, rest, workspace) as s:
         qd, kd = _packed(q), _packed(k)
         B, S, H, _ = q.shape
         out = torch.empty_like(q) if out is None else out
@@ -755,8 +756,8 @@ def window_fwd(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor |
         ws, room = _scratch(_lib.dash_attn_window_fwd_workspace_size(qd, kd), "dash_attn_window_fwd_workspace_size",
                             q.device, workspace)
         _check(_lib.dash_attn_window_fwd(qd, kd, _packed(v), _array(seqlens, "seqlens", (B,)), window, sinks,
-                                         _packed(out), _array(lse, "lse", (B, H, S), torch.float32), ws.data_ptr(),
-                                         room, s))
+                                         _packed(out), None if rest is None else _packed(rest),
+                                         _array(lse, "lse", (B, H, S), torch.float32), ws.data_ptr(), room, s))
     return (out, lse) if return_lse else out
 
 
@@ -765,40 +766,42 @@ def window_bwd_workspace_size(q: torch.Tensor, k: torch.Tensor, window: int = 0,
 
 
 def window_bwd(q, k, v, out, lse, dout, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None,
-               grads=None, workspace=None, stream=None) -> dict:
+               grads=None, rest=None, workspace=None, stream=None) -> dict:
     """Gradients of sum(dout * out) (see dash_attn_window_bwd): dq, dk, dv in the inputs' type.
 
-    out, lse: those of :func:`window_fwd`.  grads: optional dict of preallocated dq / dk / dv.
+    out, lse (and rest, if it was asked for): those of :func:`window_fwd`.  grads: optional dict of preallocated dq / dk / dv.
     """
     g = grads or {}
-    with _On(stream, q, k, v, out, lse, dout, seqlens, workspace, *g.values()) as s:
+    with _On(stream, q, k, v, out, lse, dout, seqlens, rest, workspace, *g.values()) as s:
         B, S, H, _ = q.shape
         dq, dk, dv = (g[n] if n in g else torch.empty_like(t) for n, t in (("dq", q), ("dk", k), ("dv", v)))
         qd, kd = _packed(q), _packed(k)
         ws, room = _scratch(_lib.dash_attn_window_bwd_workspace_size(qd, kd, window, sinks),
                             "dash_attn_window_bwd_workspace_size", q.device, workspace)
-        _check(_lib.dash_attn_window_bwd(qd, kd, _packed(v), _packed(out), _array(lse, "lse", (B, H, S), torch.float32),
-                                         _packed(dout), _array(seqlens, "seqlens", (B,)), window, sinks, _packed(dq),
-                                         _packed(dk), _packed(dv), ws.data_ptr(), room, s))
+        _check(_lib.dash_attn_window_bwd(qd, kd, _packed(v), _packed(out), None if rest is None else _packed(rest),
+                                         _array(lse, "lse", (B, H, S), torch.float32), _packed(dout),
+                                         _array(seqlens, "seqlens", (B,)), window, sinks, _packed(dq), _packed(dk),
+                                         _packed(dv), ws.data_ptr(), room, s))
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
 class _WindowAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, window, sinks, seqlens):
-        out, lse = window_fwd(q, k, v, window, sinks, seqlens, return_lse=True)
-        ctx.save_for_backward(q, k, v, out, lse, seqlens)
+        rest = torch.empty_like(q) if q.dtype != torch.float32 else None
+        out, lse = window_fwd(q, k, v, window, sinks, seqlens, return_lse=True, rest=rest)
+        ctx.save_for_backward(q, k, v, out, lse, rest, seqlens)
         ctx.args = (window, sinks)
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        q, k, v, out, lse, seqlens = ctx.saved_tensors
+        q, k, v, out, lse, rest, seqlens = ctx.saved_tensors
         dout = dout.contiguous()
         if dout.data_ptr() % 16:  # a view that starts between two 16-byte pieces
             dout = dout.clone()
-        g = window_bwd(q, k, v, out, lse, dout, *ctx.args, seqlens)
+        g = window_bwd(q, k, v, out, lse, dout, *ctx.args, seqlens, rest=rest)
         return g["dq"], g["dk"], g["dv"], None, None, None
 
 

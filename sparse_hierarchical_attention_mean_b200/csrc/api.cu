@@ -1377,6 +1377,12 @@ dash_status_t check_like(const dash_tensor_t* t, const dash_tensor_t* like, cons
   return DASH_OK;
 }
 
+dash_status_t check_rest(const dash_tensor_t* rest, const dash_tensor_t* q) {
+  if (!rest) return DASH_OK;
+  if (q->dtype == DASH_F32) return fail(DASH_ERR_UNSUPPORTED, "rest is for f16 and bf16");
+  return check_like(rest, q, "rest");
+}
+
 dash_status_t check_window_qk(const dash_tensor_t* q, const dash_tensor_t* k) {
   dash_status_t st;
   if ((st = check_solid(q, "q")) || (st = check_solid(k, "k")) || (st = check_group(q->h, k->h))) return st;
@@ -1457,16 +1463,18 @@ size_t dash_attn_window_fwd_workspace_size(const dash_tensor_t* q, const dash_te
 
 dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
                                    const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* out,
-                                   float* lse, void* workspace, size_t workspace_bytes, dash_stream_t stream) {
+                                   dash_tensor_t* rest, float* lse, void* workspace, size_t workspace_bytes,
+                                   dash_stream_t stream) {
   dash_status_t st;
   if ((st = check_window_qk(q, k)) || (st = check_like(v, k, "v")) || (st = check_like(out, q, "out")) ||
-      (st = check_window(window, sinks)))
+      (st = check_rest(rest, q)) || (st = check_window(window, sinks)))
     return st;
   const WindowLayout L = window_layout(q, k, window, sinks, false);
   if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
   cudaStream_t s = (cudaStream_t)stream;
   dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, lse);
-  p.wide = wide_rows(out);
+  p.wide = wide_rows(out) && (!rest || wide_rows(rest));
+  if (rest) p.rest = solid_view(rest);
   p.status = at<dash::DeviceStatus>(workspace, L.status);
   const cudaError_t e = q->dtype == DASH_F32 ? dash::launch_window_fwd_simt(p, s) : dash::launch_window_fwd_tc(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "window forward");
@@ -1480,12 +1488,13 @@ size_t dash_attn_window_bwd_workspace_size(const dash_tensor_t* q, const dash_te
 }
 
 dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* k, const dash_tensor_t* v,
-                                   const dash_tensor_t* out, const float* lse, const dash_tensor_t* dout,
-                                   const int32_t* seqlens, int64_t window, int64_t sinks, dash_tensor_t* dq,
-                                   dash_tensor_t* dk, dash_tensor_t* dv, void* workspace, size_t workspace_bytes,
-                                   dash_stream_t stream) {
+                                   const dash_tensor_t* out, const dash_tensor_t* rest, const float* lse,
+                                   const dash_tensor_t* dout, const int32_t* seqlens, int64_t window, int64_t sinks,
+                                   dash_tensor_t* dq, dash_tensor_t* dk, dash_tensor_t* dv, void* workspace,
+                                   size_t workspace_bytes, dash_stream_t stream) {
   dash_status_t st;
   if ((st = check_window_qk(q, k)) || (st = check_like(v, k, "v")) || (st = check_like(out, q, "out")) ||
+      (st = check_rest(rest, q)) ||
       (st = check_like(dout, q, "dout")) || (st = check_like(dq, q, "dq")) || (st = check_like(dk, k, "dk")) ||
       (st = check_like(dv, k, "dv")) || (st = check_window(window, sinks)))
     return st;
@@ -1494,6 +1503,7 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
   if ((st = check_workspace(workspace, workspace_bytes, L.total))) return st;
   cudaStream_t s = (cudaStream_t)stream;
   dash::WindowParams p = window_params(q, k, v, out, seqlens, window, sinks, const_cast<float*>(lse));
+  if (rest) p.rest = solid_view(rest);
   p.dout = solid_view(dout);
   p.dq = solid_view(dq);
   p.dk = solid_view(dk);

@@ -16,6 +16,7 @@ constexpr int kMaxSinks = 128;
 
 struct WindowParams {
   View q, k, v, out;        // [B, S, H or Hkv, D], dtype
+  View rest;                // [B, S, H, D], dtype: what rounding took from out; null data: none
   View dout, dq, dk, dv;    // backward, dtype
   int dtype;
   int B, S, H, Hkv, G, D;
@@ -26,7 +27,7 @@ struct WindowParams {
   // backward, tensor-core path, in the order of the row tiles (128 / G
   // positions x G heads): [B, Hkv, n_tiles, 128]
   float* nlse2;             // -lse in log2 units; -inf on rows that are not there
-  float* ndd;               // -dout . out
+  float* ndd;               // -sum_j p_ij (dout_i . v_j)
   int n_tiles;
   float* part;              // partial dk, dv of the first 128 keys [B, Hkv, n_chunks + 1, 2, 128, D]
   int n_chunks;             // items of chunk_tiles row tiles that see only sinks of the first 128 keys

@@ -8,7 +8,11 @@
 // does not depend on timing; S and dP are computed in both (7 products
 // instead of 5).  Tiles of rows are 128 = (128 / G positions) x (G heads).
 // p and dS are rounded to the input type as operands of the second products;
-// everything else is fp32.  Every wait is bounded; on expiry the status word
+// where a row sees at most kFewKeys keys, whose roundings hardly average out,
+// dq's product takes dS as the sum of two such values (window 4: dq's error is
+// 1.5 times that of rounding dq alone without, 1.1 with; the second product
+// costs the row kernel a third of its time on long windows, nothing that shows
+// on short ones).  Everything else is fp32.  Every wait is bounded; on expiry the status word
 // reads DASH_ERR_DEVICE_TIMEOUT and the roles wind down.
 #include <cuda.h>
 
@@ -40,10 +44,14 @@ constexpr int kTimeout = 5;  // DASH_ERR_DEVICE_TIMEOUT
 // tile's dq is written, so the next tile's first products overlap that.  Warp 8
 // is the TMA producer, which also clears K rows behind a sequence's end; warp 9
 // issues the MMAs.  TMEM: Q at 0, dout at D / 2, S, dP, dQ at 128, 256, 384.
+// D is dout . out and has out's rounding in it, unless `rest` brings what that
+// took.  The sum of a row's dS, which an exact D makes 0, is D's error: the key
+// kernel gets the corrected D.
 // (Steps of 64 keys in two buffers were slower: a 128 x 64 product takes the
 // tensor core 55 clocks, not 32, and S, dP and dQ of 64 keys 1100.  So were 16
 // workers of 32 keys, here and in the key kernel: 1.09 against 0.97 ms together
 // at 16K tokens, window 1024.)
+constexpr int kFewKeys = 16;
 constexpr uint32_t kColSR = 128, kColDPR = 256, kColDQ = 384;
 
 template <int D>
@@ -54,13 +62,14 @@ struct RowLayout {
   static constexpr int kOffQ = 0, kOffDo = kTile;
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffBar = kOffRing + kStages * kTile;
-  static constexpr int kOffXch = kOffBar + 512;  // [2][128] halves of D
-  static constexpr int kAlloc = kOffXch + 2 * kRows * 4;
+  static constexpr int kOffXch = kOffBar + 512;  // [2][128] halves of D, [2][128] of the row's sum of dS
+  static constexpr int kAlloc = kOffXch + 4 * kRows * 4;
 };
 
 struct RowBars {
   uint64_t rows_full, rows_empty;  // Q, dout in shared memory
   uint64_t stats;                  // both halves of D exchanged, out read
+  uint64_t sums;                   // both halves of the sums of dS
   uint64_t ready;                  // Q and dout in TMEM
   uint64_t full[10], empty[10];
   uint64_t tail;
@@ -84,11 +93,12 @@ struct RowItem {
   }
 };
 
-template <typename T, int D>
+template <typename T, int D, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     window_bwd_row_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                             const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_k,
-                             const __grid_constant__ CUtensorMap tm_v, const WindowParams p) {
+                             const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_rest,
+                             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                             const WindowParams p) {
   using L = RowLayout<D>;
   constexpr int kStages = L::kStages;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
@@ -104,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&bars->rows_full, 1);
     tc::mbar_init(&bars->rows_empty, kWorkers / 32);
     tc::mbar_init(&bars->stats, kWorkers / 32);
+    tc::mbar_init(&bars->sums, kWorkers / 32);
     tc::mbar_init(&bars->ready, kWorkers / 32);
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&bars->full[s], 1);
@@ -127,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tensormap(&tm_q);
     tc::prefetch_tensormap(&tm_do);
     tc::prefetch_tensormap(&tm_o);
+    if (p.rest.data) tc::prefetch_tensormap(&tm_rest);
     tc::prefetch_tensormap(&tm_k);
     tc::prefetch_tensormap(&tm_v);
   }
@@ -139,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // grid's end before it reads lse2 and D
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-  // ring tiles of an item: out, then K and V of each step
+  // ring tiles of an item: out (and rest), then K and V of each step
+  const int n_out = p.rest.data ? 2 : 1;
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     if (blockIdx.x == 0) begin_status(p, lane);
@@ -168,20 +181,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowItem w(p, P, it);
       it.next();
       seek();
-      for (int i = 0; ok && i <= 2 * w.steps; ++i, ++x) {
+      for (int i = 0; ok && i < n_out + 2 * w.steps; ++i, ++x) {
         const int st = x % kStages;
         if (x >= kStages) ok = warp_wait(&bars->empty[st], x / kStages - 1);
         if (!ok) break;
         uint8_t* dst = smem + L::kOffRing + st * L::kTile;
-        const int tok0 = i > 0 ? w.kt.tile((i - 1) >> 1) * kRows : 0;
-        const bool is_k = i & 1;
+        const int y = i - n_out;  // K of step y / 2, V of it
+        const int tok0 = y >= 0 ? w.kt.tile(y >> 1) * kRows : 0;
+        const bool is_k = y >= 0 && !(y & 1);
         const bool clear = is_k && tok0 + kRows > w.n && w.n < p.S;
         uint64_t* bar = clear ? &bars->tail : &bars->full[st];
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar, L::kTile);
           for (int kc = 0; kc < L::KC; ++kc) {
-            if (i == 0)
-              tc::tma_load_4d(dst + kc * L::kChunk, &tm_o, bar, kc * 64, w.g * p.G, w.pos0, w.b);
+            if (y < 0)
+              tc::tma_load_4d(dst + kc * L::kChunk, i == 0 ? &tm_o : &tm_rest, bar, kc * 64, w.g * p.G, w.pos0, w.b);
             else
               tc::tma_load_4d(dst + kc * L::kChunk, is_k ? &tm_k : &tm_v, bar, kc * 64, w.g, tok0, w.b);
           }
@@ -193,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tc::mbar_arrive(&bars->full[st]);
         }
         // the next item's rows, once this one's ring is filled
-        if (i == min(4, 2 * w.steps) && it.any()) load_rows();
+        if (i == min(4, n_out + 2 * w.steps - 1) && it.any()) load_rows();
       }
     }
     // every copy lands before the CTA retires
@@ -224,11 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowItem w(p, P, it);
       if (w.steps == 0) continue;
       auto s_of = [&](int i) {
-        const int k = x + 1 + 2 * i;
+        const int k = x + n_out + 2 * i;
         if (wait(&bars->full[k % kStages], k / kStages)) issue(kColSR, 0, k, &bars->s_full);
       };
       auto dp_of = [&](int i) {
-        const int v = x + 2 + 2 * i;
+        const int v = x + n_out + 1 + 2 * i;
         if (!wait(&bars->full[v % kStages], v / kStages)) return;
         issue(kColDPR, D / 2, v, &bars->dp_full);
         tc::mma_commit_w(&bars->empty[v % kStages]);
@@ -237,22 +251,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       s_of(0);
       if (ok) dp_of(0);
       for (int i = 0; ok && i < w.steps; ++i) {
-        const int k = x + 1 + 2 * i;
+        const int k = x + n_out + 2 * i;
         if (!wait(&bars->s_free, step + i)) break;
         if (i + 1 < w.steps) s_of(i + 1);
         if (i == 0 && items > 0) wait(&bars->dq_empty, items - 1);
         if (!ok || !wait(&bars->ds_full, step + i)) break;
-        // dQ += dS K: keys 0-63 of the operand packed at dP's column 0, 64-127 at its column 64
+        // dQ += dS K: keys 0-63 of the operand packed at dP's column 0, 64-127
+        // at its column 64, low parts 32 columns further
+#pragma unroll 1
+        for (int low = 0; low <= (kFew ? 1 : 0); ++low)
 #pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk)
-          tc::mma_f16_ts_w(tmem + kColDQ, tmem + kColDPR + (kk >> 2) * 64 + (kk & 3) * 8,
-                           rmn0 + at(k) + (uint64_t)((kk * 2048) >> 4), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kRows / 16; ++kk)
+            tc::mma_f16_ts_w(tmem + kColDQ, tmem + kColDPR + (kk >> 2) * 64 + low * 32 + (kk & 3) * 8,
+                             rmn0 + at(k) + (uint64_t)((kk * 2048) >> 4), kIdescQ,
+                             (i > 0 || kk > 0 || low > 0) ? 1u : 0u);
         if (i == w.steps - 1) tc::mma_commit_w(&bars->dq_full);
         tc::mma_commit_w(&bars->empty[k % kStages]);
         if (i + 1 < w.steps) dp_of(i + 1);
       }
       if (!ok) break;
-      x += 1 + 2 * w.steps;
+      x += n_out + 2 * w.steps;
       step += w.steps;
       ++items;
     }
@@ -302,8 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = w.pos0 + (r >> lg) < w.n;
       nlse2 = live ? -lse_next * kLog2e : kNegInf;
       ok = warp_wait(&bars->rows_full, items) && ok;
-      ok = warp_wait(&bars->full[x % kStages], x / kStages) && ok;
+      for (int y = x; y < x + n_out; ++y) ok = warp_wait(&bars->full[y % kStages], y / kStages) && ok;
       const uint8_t* po = smem + L::kOffRing + (x % kStages) * L::kTile + r * 128;
+      const uint8_t* pr = smem + L::kOffRing + ((x + 1) % kStages) * L::kTile + r * 128;
       const uint8_t* pd = smem + L::kOffDo + r * 128;
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -315,6 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         Elt<T>::to_float(*reinterpret_cast<const uint4*>(po + at), fo);
 #pragma unroll
         for (int e2 = 0; e2 < 8; ++e2) acc[e2 & 3] = fmaf(fd[e2], fo[e2], acc[e2 & 3]);
+        if (n_out > 1) {
+          Elt<T>::to_float(*reinterpret_cast<const uint4*>(pr + at), fo);
+#pragma unroll
+          for (int e2 = 0; e2 < 8; ++e2) acc[e2 & 3] = fmaf(fd[e2], fo[e2], acc[e2 & 3]);
+        }
       }
       const float mine = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       xch[half * kRows] = mine;
@@ -322,12 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&bars->stats, items) && ok;
       const float a = half == 0 ? mine : xch[0], b = half == 0 ? xch[kRows] : mine;
       ndd = live ? -(a + b) : 0.f;  // the same sum in both halves
-      if (threadIdx.x == 0) tc::mbar_arrive(&bars->empty[x % kStages]);  // every worker has read out
-      if (half == 0) {
-        const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
-        p.nlse2[at] = nlse2;
-        p.ndd[at] = ndd;
-      }
+      if (threadIdx.x == 0)  // every worker has read out
+        for (int y = x; y < x + n_out; ++y) tc::mbar_arrive(&bars->empty[y % kStages]);
     };
     // Q (half 0) and dout (half 1) into TMEM
     auto rows_to_tmem = [&] {
@@ -365,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo = pos - p.window + 1;
       // the warp's rows: first and last position
       const int pos_a = w.pos0 + ((q4 * 32) >> lg), pos_b = w.pos0 + ((q4 * 32 + 31) >> lg);
+      const float row_nlse2 = nlse2, row_ndd = ndd;
+      float2 ds_sum = make_float2(0.f, 0.f);
       for (int i = 0; i < w.steps; ++i) {
         const int y = step + i, key0 = w.kt.tile(i) * kRows + half * 64;  // the warp's keys [key0, key0 + 64)
         // none of the warp's pairs is visible, or all are
@@ -400,12 +422,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(&bars->dp_full, y))) break;
         tc::fence_after_sync();
         const float2 nd2 = make_float2(ndd, ndd);
+        [[maybe_unused]] uint32_t low[2][16];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t dw[16];
           if (none) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) dw[j] = 0u;
+            for (int j = 0; j < 16; ++j) {
+              dw[j] = 0u;
+              if constexpr (kFew) low[c][j] = 0u;
+            }
           } else {
             uint32_t dv[32];
             tc::tmem_ld32(d_tm + c * 32, dv);
@@ -429,21 +455,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) dw[j] = pack2<T>(ds[j].x, ds[j].y);
+            for (int j = 0; j < 16; j += 4) {
+              ds_sum = __fadd2_rn(ds_sum, __fadd2_rn(__fadd2_rn(ds[j], ds[j + 1]), __fadd2_rn(ds[j + 2], ds[j + 3])));
+#pragma unroll
+              for (int u = 0; u < 4; ++u) dw[j + u] = pack2<T>(ds[j + u].x, ds[j + u].y);
+              if constexpr (kFew) {
+                float hi[8];
+                Elt<T>::to_float(make_uint4(dw[j], dw[j + 1], dw[j + 2], dw[j + 3]), hi);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  low[c][j + u] = pack2<T>(ds[j + u].x - hi[2 * u], ds[j + u].y - hi[2 * u + 1]);
+              }
+            }
           }
           tc::tmem_st16(d_tm + c * 16, dw);
+        }
+        if constexpr (kFew) {  // over columns whose dP has been read
+          tc::tmem_st16(d_tm + 32, low[0]);
+          tc::tmem_st16(d_tm + 48, low[1]);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         warp_arrive(&bars->ds_full, lane);
       }
       step += w.steps;
-      x += 1 + 2 * w.steps;
+      x += n_out + 2 * w.steps;
       const int item = items++;
+      xch[(2 + half) * kRows] = ds_sum.x + ds_sum.y;
+      warp_arrive(&bars->sums, lane);
       if (more) row_stats(it);  // (while the last dQ runs)
       if (!ok || !(ok = warp_wait(&bars->dq_full, item))) break;
       tc::fence_after_sync();
       if (more) rows_to_tmem();
+      // ---- for the key kernel: -lse2 and -D, corrected by the sum of dS
+      if (!(ok = warp_wait(&bars->sums, item))) break;
+      if (half == 0) {
+        const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
+        p.nlse2[at] = row_nlse2;
+        p.ndd[at] = pos < w.n ? row_ndd - (xch[2 * kRows] + xch[3 * kRows]) : 0.f;
+      }
       // ---- dq of the item, each half of the workers takes half of the columns
       const bool live = pos < w.n;
       T* dst = static_cast<T*>(const_cast<void*>(p.dq.data)) + (int64_t)w.b * p.dq.sb +
@@ -927,19 +977,21 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
   const int64_t key_items = ((int64_t)(p.S + kRows - 1) / kRows + p.n_chunks) * p.Hkv * p.B;
   if (std::max(row_items, key_items) > 0x7fffffff - 4096) return cudaErrorInvalidValue;
   cudaError_t e;
-  CUtensorMap mq, mdo, mo, mk, mv;
+  CUtensorMap mq, mdo, mo, mr, mk, mv;
   if (!window_map(&mq, p.q, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
       !window_map(&mdo, p.dout, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
       !window_map(&mo, p.out, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
+      !window_map(&mr, p.rest.data ? p.rest : p.out, p.dtype, p.B, p.S, p.H, D, p.G, P) ||
       !window_map(&mk, p.k, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows) ||
       !window_map(&mv, p.v, p.dtype, p.B, p.S, p.Hkv, D, 1, kRows))
     return cudaErrorInvalidValue;
   {
     using L = RowLayout<D>;
-    auto kern = window_bwd_row_tc_kernel<T, D>;
+    auto kern = p.window + p.sinks <= kFewKeys ? window_bwd_row_tc_kernel<T, D, true>
+                                               : window_bwd_row_tc_kernel<T, D, false>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
-    kern<<<(unsigned)std::min<int64_t>(row_items, p.num_sms), kThreads, L::kAlloc, stream>>>(mq, mdo, mo, mk, mv, p);
+    kern<<<(unsigned)std::min<int64_t>(row_items, p.num_sms), kThreads, L::kAlloc, stream>>>(mq, mdo, mo, mr, mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   {

@@ -379,7 +379,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) ov[j] = 0u;
         }
-        if (pos < p.S) store_row32(dst + cc * 32, ov, inv, p.wide);
+        if (pos < p.S) {
+          store_row32(dst + cc * 32, ov, inv, p.wide);
+          if (p.rest.data) {
+            rounding_rest<T>(ov, inv);
+            T* rest = static_cast<T*>(const_cast<void*>(p.rest.data)) + (int64_t)w.b * p.rest.sb +
+                      (int64_t)pos * p.rest.ss + (int64_t)head * p.rest.sh;
+            store_row32(rest + cc * 32, ov, 1.f, p.wide);
+          }
+        }
       }
       if (w.steps > 0) {
         tc::fence_before_sync();

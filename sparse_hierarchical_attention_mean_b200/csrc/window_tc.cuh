@@ -118,6 +118,18 @@ __device__ __forceinline__ void store_row32(T* dst, const uint32_t* v, float sca
   }
 }
 
+// v <- what is left of v * scale when it is rounded to T.
+template <typename T>
+__device__ __forceinline__ void rounding_rest(uint32_t* v, float scale) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    float f[8];
+    Elt<T>::to_float(pack8<T>(v + j, scale), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[j + e] = __float_as_uint(fmaf(__uint_as_float(v[j + e]), scale, -f[e]));
+  }
+}
+
 // Zeroes rows [row0, rows) of a tile of 64-column chunks ([rows][128 bytes]
 // each; the 128-byte swizzle moves bytes within a row only) and makes that
 // visible to the tensor core.  Called by one converged warp.

@@ -59,34 +59,38 @@ def lse_bound(f, d, dtype):
 
 
 def backward(q, k, v, out, dout, f):
-    """One head: gradients with D = dout . out from the given out, their magnitude sums and root sums of squares."""
+    """One head: gradients, their magnitude sums and root sums of squares.  dq has D = dout . out from the given out
+    (the forward's, with the rest of its rounding or without); for dk and dv D is that of the definition."""
     scale = 1 / math.sqrt(q.shape[-1])
     p = f["p"]
     dp = dout @ v.T
-    delta = (dout * out).sum(-1, keepdim=True)
-    ds = p * (dp - delta)
+    ds_q = p * (dp - (dout * out).sum(-1, keepdim=True))
+    ds = p * (dp - (dout * f["out"]).sum(-1, keepdim=True))
     ads, p2, ds2 = ds.abs(), p * p, ds * ds
     # fp32 sums behind dS: dp and D are sums of d products each
     slack = p * (dout.abs() @ v.abs().T + (dout * out).abs().sum(-1, keepdim=True))
     # f16 operands below 2^-14 lie on multiples of 2^-24: half a step each
     w = (p > 0).double() * 2.0 ** -25
     return dict(dq_sub=w @ k.abs() * scale, dk_sub=w.T @ q.abs() * scale, dv_sub=w.T @ dout.abs(),
-                dq=ds @ k * scale, dq_abs=ads @ k.abs() * scale, dq_rss=(ds2 @ (k * k)).sqrt() * scale,
-                dq_slack=slack @ k.abs() * scale,
+                dq=ds_q @ k * scale, dq_abs=ds_q.abs() @ k.abs() * scale, dq_slack=slack @ k.abs() * scale,
+                dq_sq=(ds_q * ds_q) @ (k * k) * scale ** 2,
+                dk_d=(p * (p * dp.abs()).sum(-1, keepdim=True)).T @ q.abs() * scale,
                 dk=ds.T @ q * scale, dk_abs=ads.T @ q.abs() * scale, dk_sq=(ds2.T @ (q * q)) * scale ** 2,
                 dk_slack=slack.T @ q.abs() * scale,
                 dv=p.T @ dout, dv_abs=p.T @ dout.abs(), dv_sq=p2.T @ (dout * dout), dv_slack=torch.zeros_like(v))
 
 
-def grad_bound(g, name, rel, dtype, d):
+def grad_bound(g, name, rel, dtype, d, few=False):
     """P (for dv) and dS (for dq, dk) are rounded once as operands, unbiased and independent: a standard deviation of
-    u / sqrt(3) times the root sum of squares of the terms; 3.5 u of it is six of those.  rel: how far the fp32
-    arithmetic may move each p (the largest over the rows); dp and D carry (d + 8) 2^-24 of their magnitudes."""
+    u / sqrt(3) times the root sum of squares of the terms; 3.5 u of it is six of those.  Where a row sees few keys
+    (at most 16), dS for dq is two such values: u^2 of each term.  rel: how far the fp32 arithmetic may move each p (the largest over the rows); it moves the D of
+    dk, a sum of p dp, too; dp and D carry (d + 8) 2^-24 of their magnitudes."""
     u = ROUNDOFF[dtype]
-    rss = g[name + "_sq"].sqrt() if name + "_sq" in g else g[name + "_rss"]
     bound = u * g[name].abs() + (rel + 2.0 ** -20) * g[name + "_abs"] + 2 * (d + 8) * 2.0 ** -24 * g[name + "_slack"]
+    if name == "dk":
+        bound = bound + rel * g["dk_d"]
     if dtype != torch.float32:
-        bound = bound + 3.5 * u * rss
+        bound = bound + (u * u * g["dq_abs"] if name == "dq" and few else 3.5 * u * g[name + "_sq"].sqrt())
     if dtype == torch.float16:
         bound = bound + g[name + "_sub"] + 2.0 ** -25
     return bound + 1e-7 * float(g[name + "_abs"].max().clamp(min=0)) + 1e-30

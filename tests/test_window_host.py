@@ -20,14 +20,14 @@ def _ref(*tensors):
     return [ctypes.byref(t) for t in tensors]
 
 
-def _fwd(q, k, v, o, window=64, sinks=4, ws=FAKE, ws_bytes=BIG):
-    return dash.load().dash_attn_window_fwd(*_ref(q, k, v), None, window, sinks, ctypes.byref(o), None, ws, ws_bytes,
-                                            None)
+def _fwd(q, k, v, o, window=64, sinks=4, ws=FAKE, ws_bytes=BIG, rest=None):
+    return dash.load().dash_attn_window_fwd(*_ref(q, k, v), None, window, sinks, ctypes.byref(o),
+                                            rest and ctypes.byref(rest), None, ws, ws_bytes, None)
 
 
-def _bwd(q, k, v, o, do, dq, dk, dv, window=64, sinks=4, lse=FAKE, ws=FAKE, ws_bytes=BIG):
-    return dash.load().dash_attn_window_bwd(*_ref(q, k, v, o), lse, ctypes.byref(do), None, window, sinks,
-                                            *_ref(dq, dk, dv), ws, ws_bytes, None)
+def _bwd(q, k, v, o, do, dq, dk, dv, window=64, sinks=4, lse=FAKE, ws=FAKE, ws_bytes=BIG, rest=None):
+    return dash.load().dash_attn_window_bwd(*_ref(q, k, v, o), rest and ctypes.byref(rest), lse, ctypes.byref(do), None,
+                                            window, sinks, *_ref(dq, dk, dv), ws, ws_bytes, None)
 
 
 def _good():
@@ -81,6 +81,12 @@ def test_window_range_and_workspace():
     assert need >= 8 * 256 * 4
     assert _bwd(*_good_bwd(), ws_bytes=need - 1) == 3
     assert _bwd(*_good_bwd(), lse=None) == 1 and "lse" in _error()
+    for rest in (tensor(1, 256, 8, 128, dtype=1), tensor(1, 255, 8, 128), tensor(1, 256, 8, 128, data=FAKE + 4)):
+        assert _fwd(*_good(), rest=rest) == 1 and "rest" in _error()
+        assert _bwd(*_good_bwd(), rest=rest) == 1 and "rest" in _error()
+    fp32 = [tensor(1, 256, h, 128, dtype=0) for h in (8, 2, 2, 8, 8, 8, 2, 2)]
+    assert _fwd(*fp32[:4], rest=fp32[3]) == 2 and "rest" in _error()
+    assert _bwd(*fp32, rest=fp32[3]) == 2 and "rest" in _error()
     for i in (4, 5, 6, 7):
         args = _good_bwd()
         args[i].dtype = 0
