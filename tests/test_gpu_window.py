@@ -278,6 +278,32 @@ def test_captured_and_replayed(cuda_lib):
     assert all(torch.equal(grads[n], want[n]) for n in want)
 
 
+def test_captured_training_step(cuda_lib):
+    """Forward and gradients through autograd in one graph, of leaves that no eager graph holds."""
+    dash = cuda_lib
+    case = (1, 300, 4, 2, 64, F16, 60, 3, None)
+    q, k, v, do, _ = _inputs(case, 5)
+    leaves = [t.requires_grad_(True) for t in (q, k, v)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(dash.window_attention(*leaves, window=60, sinks=3), leaves, do)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dash.window_attention(*leaves, window=60, sinks=3)
+        grads = torch.autograd.grad(out, leaves, do)
+    with torch.no_grad():
+        for a, b in zip((q, k, v, do), _inputs(case, 6)):
+            a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    leaves = [t.detach().requires_grad_(True) for t in leaves]
+    eager = dash.window_attention(*leaves, window=60, sinks=3)
+    want = torch.autograd.grad(eager, leaves, do)
+    assert torch.equal(out, eager) and all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
 def test_other_stream(cuda_lib):
     """Buffers that the call makes belong to the stream it runs on, also while another stream is current."""
     dash = cuda_lib
