@@ -442,7 +442,8 @@ dash_status_t dash_attn_sparse_mask(const dash_tensor_t* q, const dash_tensor_t*
  *            logits; NULL in the forward if not wanted.  The backward reads
  *            the forward's.
  * Strides of 0 over an extent above 1 are refused (DASH_ERR_UNSUPPORTED).
- * Outputs must not overlap inputs.
+ * Outputs must not overlap inputs.  Calls that may run at the same time need
+ * a workspace each (also below).
  */
 
 /* Bytes of workspace of dash_attn_window_fwd (a status word). 0: rejected arguments. */

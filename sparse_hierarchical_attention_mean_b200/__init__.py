@@ -806,7 +806,13 @@ class _WindowAttention(torch.autograd.Function):
 
 
 def window_attention(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None) -> torch.Tensor:
-    """Differentiable :func:`window_fwd`: forward by dash_attn_window_fwd, gradients by dash_attn_window_bwd."""
+    """Differentiable :func:`window_fwd`: forward by dash_attn_window_fwd, gradients by dash_attn_window_bwd.
+
+    In a captured step, as for any operator of torch, the leaves must have no eager graph alive when the capture
+    starts: the gradients would be accumulated on the stream of that graph, outside the capture.
+    """
+    if not torch.is_grad_enabled():  # nothing to keep for a backward
+        return window_fwd(q, k, v, window, sinks, seqlens)
     return _WindowAttention.apply(q, k, v, window, sinks, seqlens)
 
 

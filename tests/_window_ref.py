@@ -6,8 +6,7 @@ length are not there.
 Rounding model.  u is the unit roundoff of the inputs' type (half a step: bf16 2^-8, f16 2^-11, f32 2^-24).
   logits   fp32 sums of d products: |error| <= (d + 8) 2^-24 M, M = max_j sum_e |q_e k_je| / sqrt(d) (the 8 covers
            the scale and the subtraction of the reference); p and the row sum each move by that relative amount
-  exp      2^-15 relative on the tensor-core path (the published polynomial bound plus the special-function unit's),
-           2^-20 on the fp32 path
+  exp      2^-20 relative (the special-function unit's 2^x is within 2^-22)
   sums     n visible terms in fp32: n 2^-24 relative to the sum of magnitudes
   P        rounded to the inputs' type as an operand (not on the fp32 path): u relative
   out      rounded once: u |out|
@@ -41,7 +40,7 @@ def forward(q, k, v, seen):
 
 def moved(f, d, dtype):
     """Relative amount by which the fp32 arithmetic may move each p of a row."""
-    exp = 2.0 ** -20 if dtype == torch.float32 else 2.0 ** -15
+    exp = 2.0 ** -20
     return (2 * (d + 8) * f["mag"] + 2 * f["count"]) * 2.0 ** -24 + exp
 
 

@@ -304,6 +304,19 @@ def test_captured_training_step(cuda_lib):
     assert torch.equal(out, eager) and all(torch.equal(a, b) for a, b in zip(grads, want))
 
 
+def test_without_gradients(cuda_lib):
+    """The differentiable form under no_grad: the forward's bits, nothing kept; transposed inputs keep their layout."""
+    dash = cuda_lib
+    case = (2, 200, 4, 2, 64, F16, 60, 3, None)
+    q, k, v, _, _ = _inputs(case, 9)
+    want = dash.window_attention(q.requires_grad_(True), k, v, 60, 3)
+    with torch.no_grad():
+        out = dash.window_attention(q, k, v, 60, 3)
+        t = dash.window_fwd(q.transpose(1, 2).contiguous().transpose(1, 2), k, v, 60, 3)
+    assert want.requires_grad and not out.requires_grad and torch.equal(out, want)
+    assert torch.equal(t, want) and t.transpose(1, 2).is_contiguous()
+
+
 def test_other_stream(cuda_lib):
     """Buffers that the call makes belong to the stream it runs on, also while another stream is current."""
     dash = cuda_lib
