@@ -785,6 +785,14 @@ def window_bwd(q, k, v, out, lse, dout, window: int = 0, sinks: int = 0, seqlens
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
+def _readable(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy of it where its strides or its address are not ones that the kernels read."""
+    *outer, last = t.stride()
+    if last == 1 and all(x > 0 and x * t.element_size() % 16 == 0 for x in outer) and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class _WindowAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, window, sinks, seqlens):
@@ -798,10 +806,7 @@ class _WindowAttention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, rest, seqlens = ctx.saved_tensors
-        dout = dout.contiguous()
-        if dout.data_ptr() % 16:  # a view that starts between two 16-byte pieces
-            dout = dout.clone()
-        g = window_bwd(q, k, v, out, lse, dout, *ctx.args, seqlens, rest=rest)
+        g = window_bwd(q, k, v, out, lse, _readable(dout), *ctx.args, seqlens, rest=rest)
         return g["dq"], g["dk"], g["dv"], None, None, None
 
 

@@ -22,9 +22,8 @@
 // G <= 8 query heads are the rows of a warp-level m16n8k16 MMA (half of it is
 // padding: the products need 1% of the tensor rate, the 64-row minimum of
 // tcgen05 would waste eight times that).  P is rounded to the cache's type
-// for the second product (as FlashAttention-like kernels do: relative error
-// half a step of that type per term, averaged over the sum); m, l and o are
-// fp32.
+// for the second product, the MMA's operand type (relative error half a step
+// of that type per term, averaged over the sum); m, l and o are fp32.
 //
 // What stands in the cache at masked tokens is never used: masked logits are
 // replaced before the maximum, and masked V values are cleared in registers

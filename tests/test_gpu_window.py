@@ -218,6 +218,13 @@ def test_autograd(cuda_lib, dtype):
     assert odd.data_ptr() % 16 != 0
     (gk,) = torch.autograd.grad(dash.window_attention(q, k, v, 40, 3, seqlens), k, odd)
     assert torch.equal(gk, want["dk"])
+    # one in another order of dimensions, and one whose rows are 65 elements apart
+    turned = do.transpose(1, 2).contiguous().transpose(1, 2)
+    wide = torch.nn.functional.pad(do, (0, 1))[..., :64]
+    assert not turned.is_contiguous() and wide.stride(2) == 65
+    for d in (turned, wide):
+        got = torch.autograd.grad(dash.window_attention(q, k, v, 40, 3, seqlens), (q, k, v), d)
+        assert all(torch.equal(a, want[n]) for a, n in zip(got, ("dq", "dk", "dv")))
     # one that is a broadcast view
     total = dash.window_attention(q, k, v, 40, 3, seqlens).sum()
     (gq,) = torch.autograd.grad(total, q)
