@@ -44,7 +44,6 @@ namespace {
 constexpr int kStep = 64;
 constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kWholeSteps = 8;  // parts up to this long are whole steps
 constexpr int kPairSteps = 2;   // steps of pairs of heads a CTA gets at least, or heads go one by one
 
 template <int D, int HP>
@@ -99,25 +98,20 @@ __device__ __forceinline__ void batch_steps(const WindowDecodeParams& p, int b, 
   if (before) *before = warp_sum_ll(f);
 }
 
-// How the line of `units` steps is cut into n parts.  Short parts have whole
-// steps, `per` each and maybe fewer in the last: the longest is no longer than
-// with n_cta equal parts, and more cuts fall between two units, which saves a
-// CTA a second merge (512 steps of 32 units: 9.3 us instead of 10.2; one
-// sequence of 1792 tokens: parts of 2 steps 8.3, of 4 9.2).  Long ones are
-// equal, so that every SM streams to the end (3 x 9024 tokens: 26.4 us, whole
-// steps 27.1).  Part c is [c line / n, (c + 1) line / n).
+// How the line of `units` steps is cut: n parts of `per` whole steps each, the
+// last maybe shorter.  No part is longer than with n_cta equal parts (which
+// end within a step of each other too), and more cuts fall between two units,
+// which saves a CTA a second merge: 512 steps of 32 units 9.3 us instead of
+// 10.2; long lines gained up to 4% in a graph, nothing on cold caches.  At least 2 or 4 steps
+// a part (fewer partials to join) were slower: one sequence of 1792 tokens 8.3
+// us with 2, 9.2 with 4; of 640 tokens 7.0 with 1, 7.4 with 2.
 struct Cut {
-  long long units, line;  // line: units, made up to n whole parts
+  long long units, per;
   int n;
-  __device__ Cut(long long u, int n_cta) : units(u), line(u), n(n_cta) {
-    const long long per = max(1ll, (u + n_cta - 1) / n_cta);
-    if (per <= kWholeSteps) {
-      n = (int)max(1ll, (u + per - 1) / per);
-      line = n * per;
-    }
-  }
-  __device__ long long start(int c) const { return min(units, line * c / n); }
-  __device__ int owner(long long u) const { return (int)(((u + 1) * n - 1) / line); }
+  __device__ Cut(long long u, int n_cta)
+      : units(u), per(max(1ll, (u + n_cta - 1) / n_cta)), n((int)((u + per - 1) / per)) {}
+  __device__ long long start(int c) const { return min(units, per * c); }
+  __device__ int owner(long long u) const { return (int)(u / per); }
 };
 
 // Walks a part of the line: the (sequence, KV head or pair of them) segments in
@@ -484,7 +478,8 @@ __global__ void __launch_bounds__(kJoinThreads) window_decode_join_kernel(const 
     if (i0 < parts && e0 < G * D) {
 #pragma unroll
       for (int i = i0; i < i0 + 8; ++i)
-        ahead[i] = i < parts ? *reinterpret_cast<const float2*>(p.part_o + slot(i) * G * D + e0) : make_float2(0.f, 0.f);
+        ahead[i] = i < parts ? *reinterpret_cast<const float2*>(p.part_o + slot(i) * G * D + e0)
+                             : make_float2(0.f, 0.f);
     }
   for (int h = warp; h < G; h += kJoinThreads / 32) {
     float l = 0.f;
