@@ -62,7 +62,9 @@ struct RowLayout {
   static constexpr int kOffQ = 0, kOffDo = kTile;
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffBar = kOffRing + kStages * kTile;
-  static constexpr int kOffXch = kOffBar + 512;  // [2][128] halves of D, [2][128] of the row's sum of dS
+  // exchange between the halves of the workers: [2][128] their halves of D,
+  // [2][128] half 1's sum of a row's dS, of even and of odd items
+  static constexpr int kOffXch = kOffBar + 512;
   static constexpr int kAlloc = kOffXch + 4 * kRows * 4;
 };
 
@@ -481,7 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       step += w.steps;
       x += n_out + 2 * w.steps;
       const int item = items++;
-      xch[(2 + half) * kRows] = ds_sum.x + ds_sum.y;
+      // Half 0 reads half 1's sum after it has let the next item start, and
+      // nothing holds that item's workers back when it has one step: the next
+      // sum goes to the other slot.  The one after it comes back to this slot
+      // only once half 0 has handed over that item's rows, after its read.
+      const float my_sum = ds_sum.x + ds_sum.y;
+      float* const sum1 = xch + (2 + (item & 1)) * kRows;
+      if (half == 1) *sum1 = my_sum;
       warp_arrive(&bars->sums, lane);
       if (more) row_stats(it);  // (while the last dQ runs)
       if (!ok || !(ok = warp_wait(&bars->dq_full, item))) break;
@@ -492,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (half == 0) {
         const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
         p.nlse2[at] = row_nlse2;
-        p.ndd[at] = pos < w.n ? row_ndd - (xch[2 * kRows] + xch[3 * kRows]) : 0.f;
+        p.ndd[at] = pos < w.n ? row_ndd - (my_sum + *sum1) : 0.f;
       }
       // ---- dq of the item, each half of the workers takes half of the columns
       const bool live = pos < w.n;
