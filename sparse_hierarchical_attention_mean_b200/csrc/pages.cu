@@ -378,9 +378,15 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (at[k] >= 0) *reinterpret_cast<uint4*>(to + at[k]) = v[k];
 }
 
-cudaError_t launch(void (*kern)(const PagesParams), size_t smem, const PagesParams& p, cudaStream_t stream) {
+// `rows` rows of `row` bytes of shared memory.  The kernel's limit is state that
+// all host threads share, so it is always set to that of the largest call: set
+// to each call's own size, another thread's smaller one could come between it
+// and the launch, which then failed.
+cudaError_t launch(void (*kern)(const PagesParams), int64_t rows, int row, const PagesParams& p, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = (size_t)rows * row;
+  if (smem > 40 * 1024)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPageSlots * row);
   if (e != cudaSuccess) return e;
   kern<<<kCtas, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
@@ -389,13 +395,13 @@ cudaError_t launch(void (*kern)(const PagesParams), size_t smem, const PagesPara
 }  // namespace
 
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
-  return launch(pages_fork_kernel, (size_t)p.n * 16, p, stream);
+  return launch(pages_fork_kernel, p.n, 16, p, stream);
 }
 cudaError_t launch_pages_grow(const PagesParams& p, cudaStream_t stream) {
-  return launch(pages_grow_kernel, (size_t)p.batch * 8, p, stream);
+  return launch(pages_grow_kernel, p.batch, 8, p, stream);
 }
 cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t stream) {
-  return launch(pages_compact_kernel, 0, p, stream);
+  return launch(pages_compact_kernel, 0, 0, p, stream);
 }
 
 static int64_t copy_chunks(const PageCopyParams& p) {
