@@ -901,12 +901,19 @@ def pages_free(block_table, seqlens, refs, slots, block: int, workspace=None, st
         _check(_lib.dash_attn_pages_free(*state, _array(slots, "slots", (n,)), n, block, ws.data_ptr(), room, s))
 
 
-def pages_grow(block_table, seqlens, refs, n_new, block: int, workspace=None, stream=None):
+class Grown(tuple):
+    """copy_src, copy_dst of :func:`pages_grow`, with the workspace whose status word says whether the pool sufficed."""
+
+    workspace: torch.Tensor
+
+
+def pages_grow(block_table, seqlens, refs, n_new, block: int, workspace=None, stream=None) -> Grown:
     """Room for n_new[b] more tokens of every sequence, in place (see dash_attn_pages_grow).
 
     Returns copy_src, copy_dst [batch]: the page copies to make with :func:`pages_copy` before the new tokens are
-    written (-1: none).  When the pool has too few free pages nothing changes; pass a workspace to read that from
-    :func:`device_status`.
+    written (-1: none).  When the pool has too few free pages nothing changes, the lengths neither, and
+    ``device_status(result.workspace)`` is 6 (DASH_ERR_OUT_OF_PAGES): where the pool can run out, look at it before
+    the tokens are written (it synchronises), or count the free pages beforehand.
     """
     with _On(stream, block_table, seqlens, refs, n_new, workspace) as s:
         state = _pages_state(block_table, seqlens, refs)
@@ -915,7 +922,9 @@ def pages_grow(block_table, seqlens, refs, n_new, block: int, workspace=None, st
         ws, room = _pages_scratch(state, block_table.device, workspace)
         _check(_lib.dash_attn_pages_grow(*state, _array(n_new, "n_new", (batch,)), block, src.data_ptr(),
                                          dst.data_ptr(), ws.data_ptr(), room, s))
-    return src, dst
+    grown = Grown((src, dst))
+    grown.workspace = ws
+    return grown
 
 
 def pages_compact(block_table, seqlens, refs, block: int, inplace: bool = False, workspace=None, stream=None) -> dict:

@@ -5,7 +5,8 @@ import threading
 import pytest
 import torch
 
-from tests.test_gpu_pages import _dev
+from tests._pages_model import Pool
+from tests.test_gpu_pages import _dev, _same, _state, _ws
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,23 @@ def test_threads_with_tables_of_different_sizes(cuda_lib):
     for t in threads:
         t.join()
     assert failed == {8192: 0, 5300: 0}
+
+
+def test_a_pool_that_runs_out_is_seen(cuda_lib):
+    """Growing without a workspace of one's own: the result says whether the sequences grew."""
+    dash = cuda_lib
+    m = Pool(3, 4, 4, 64)
+    m.grow([100, 64, 0])
+    table, seqlens, refs = _state(m)
+    grown = dash.pages_grow(table, seqlens, refs, _dev([0, 0, 65]), 64)
+    assert dash.device_status(grown.workspace) == 6
+    _same(m, table, seqlens, refs)
+    src, dst = grown
+    assert (src == -1).all() and (dst == -1).all()
+    want = m.grow([0, 0, 64])
+    grown = dash.pages_grow(table, seqlens, refs, _dev([0, 0, 64]), 64)
+    assert dash.device_status(grown.workspace) == 0
+    assert [t.tolist() for t in grown] == list(want)
+    _same(m, table, seqlens, refs)
+    ws = _ws(dash, m)
+    assert dash.pages_grow(table, seqlens, refs, _dev([0, 0, 0]), 64, workspace=ws).workspace is ws
