@@ -523,8 +523,9 @@ dash_status_t dash_attn_window_decode_paged(const dash_tensor_t* q, const dash_t
  *                entries are not read.
  *   seqlens      int32 [batch].
  *   refs         int32 [n_pages]: how many table entries hold each page
- *                (entries of other tables or owners may be counted too); a
- *                page is free when this is 0.
+ *                (entries of other tables or owners may be counted too:
+ *                such a page is never handed out, but compacting moves it);
+ *                a page is free when this is 0.
  * One table serves the pools of all layers.  The calls only touch this state;
  * dash_attn_pages_copy moves the pages' contents.  New pages are the lowest
  * free ones, so every call is a function of the state.  Each call is one
@@ -572,7 +573,10 @@ dash_status_t dash_attn_pages_grow(int32_t* block_table, int64_t batch, int64_t 
 
 /*
  * Pages to the low end of the pool: with `held` pages in use, the i-th used
- * page at or past `held` moves to the i-th free one below it.
+ * page at or past `held` moves to the i-th free one below it, whoever holds
+ * it.  Only the given table is renumbered: other tables and owners that refs
+ * counts have to be by the caller, from the list of moves (an entry equal to
+ * move_src[i] becomes move_dst[i]).
  *   table_out, refs_out  the state after it (may be the inputs themselves);
  *                entries past a sequence's blocks are copied as they are.
  *   move_src, move_dst   device int32 [n_pages / 2]: the moves to make with

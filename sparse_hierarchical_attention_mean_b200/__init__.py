@@ -931,7 +931,8 @@ def pages_compact(block_table, seqlens, refs, block: int, inplace: bool = False,
     """The pages in use move to the low end of the pool (see dash_attn_pages_compact).
 
     Returns table and refs after it (the inputs themselves with ``inplace``), the moves src, dst [n_pages // 2] to
-    make with :func:`pages_copy` (-1 past their number) and info [2] = {moves, pages in use}.
+    make with :func:`pages_copy` (-1 past their number) and info [2] = {moves, pages in use}.  Pages that other tables
+    or owners hold (counted in refs) move too: their entries equal to src[i] have to become dst[i].
     """
     with _On(stream, block_table, seqlens, refs, workspace) as s:
         state = _pages_state(block_table, seqlens, refs)

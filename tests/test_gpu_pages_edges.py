@@ -61,3 +61,33 @@ def test_a_pool_that_runs_out_is_seen(cuda_lib):
     _same(m, table, seqlens, refs)
     ws = _ws(dash, m)
     assert dash.pages_grow(table, seqlens, refs, _dev([0, 0, 0]), 64, workspace=ws).workspace is ws
+
+
+def test_compaction_beside_another_owner(cuda_lib):
+    """Pages that a second table holds move too; its entries follow by the list of moves."""
+    dash, block = cuda_lib, 64
+    gen = torch.Generator().manual_seed(3)
+    ids = torch.randperm(40, generator=gen)
+    mine, other = torch.full((2, 5), -1, dtype=torch.int32), torch.full((3, 4), -1, dtype=torch.int32)
+    mine[0, :4], mine[1, :5] = ids[:4], ids[4:9]
+    other[0, :3], other[1, :2] = ids[9:12], ids[12:14]
+    other[2, :2] = mine[0, :2]  # a prefix that both hold
+    refs = torch.zeros(40, dtype=torch.int32)
+    for t in (mine, other):
+        refs += torch.bincount(t[t >= 0].long(), minlength=40).to(torch.int32)
+    pool = torch.randn(40, block, 1, 64, device="cuda")
+    mine, other, refs, seqlens = mine.cuda(), other.cuda(), refs.cuda(), _dev([4 * block, 5 * block])
+
+    def contents(table):
+        return pool[table[table >= 0].long()]
+
+    before = contents(mine), contents(other)
+    moved = dash.pages_compact(mine, seqlens, refs, block, inplace=True)
+    dash.pages_copy([pool], moved["src"], moved["dst"])
+    src, dst = (moved[n][:int(moved["info"][0])].long() for n in ("src", "dst"))
+    to = torch.arange(40, device="cuda", dtype=torch.int32)
+    to[src] = dst.to(torch.int32)
+    other = torch.where(other >= 0, to[other.clamp(min=0).long()], other)
+    assert int(mine.max()) < 14 and int(other.max()) < 14 and int(moved["info"][1]) == 14
+    assert torch.equal(contents(mine), before[0]) and torch.equal(contents(other), before[1])
+    assert int(refs[:14].min()) == 1 and int(refs[14:].max()) == 0 and torch.equal(other[2, :2], mine[0, :2])
