@@ -18,6 +18,7 @@ import os
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdashattn.so")
 
@@ -811,12 +812,13 @@ class _WindowAttention(torch.autograd.Function):
 
 
 def window_attention(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None) -> torch.Tensor:
-    """Differentiable :func:`window_fwd`: forward by dash_attn_window_fwd, gradients by dash_attn_window_bwd.
+    """Differentiable :func:`window_fwd` (reverse mode): forward by dash_attn_window_fwd, gradients by dash_attn_window_bwd.
 
     In a captured step, as for any operator of torch, the leaves must have no eager graph alive when the capture
     starts: the gradients would be accumulated on the stream of that graph, outside the capture.
     """
-    if not torch.is_grad_enabled():  # nothing to keep for a backward
+    # without gradients there is nothing to keep for a backward; a tangent is the function's to refuse
+    if not torch.is_grad_enabled() and not any(forward_ad.unpack_dual(t).tangent is not None for t in (q, k, v)):
         return window_fwd(q, k, v, window, sinks, seqlens)
     return _WindowAttention.apply(q, k, v, window, sinks, seqlens)
 
