@@ -797,6 +797,8 @@ def _readable(t: torch.Tensor) -> torch.Tensor:
 class _WindowAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, window, sinks, seqlens):
+        if not any(ctx.needs_input_grad[:3]):
+            return window_fwd(q, k, v, window, sinks, seqlens)
         rest = torch.empty_like(q) if q.dtype != torch.float32 else None
         out, lse = window_fwd(q, k, v, window, sinks, seqlens, return_lse=True, rest=rest)
         ctx.save_for_backward(q, k, v, out, lse, rest, seqlens)
@@ -812,7 +814,7 @@ class _WindowAttention(torch.autograd.Function):
 
 
 def window_attention(q, k, v, window: int = 0, sinks: int = 0, seqlens: torch.Tensor | None = None) -> torch.Tensor:
-    """Differentiable :func:`window_fwd` (reverse mode): forward by dash_attn_window_fwd, gradients by dash_attn_window_bwd.
+    """Differentiable :func:`window_fwd` (reverse mode): by dash_attn_window_fwd and dash_attn_window_bwd.
 
     In a captured step, as for any operator of torch, the leaves must have no eager graph alive when the capture
     starts: the gradients would be accumulated on the stream of that graph, outside the capture.

@@ -34,3 +34,21 @@ def test_a_tangent_is_never_dropped(asked, grad_mode, which):
         args[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
         with pytest.raises(NotImplementedError):
             dash.window_attention(*args, 4)
+
+
+def test_nothing_is_kept_when_no_input_asks_for_a_gradient(asked):
+    """The log-sum-exp and what rounding took are made for a backward only."""
+    q, k, v = _qkv()
+    out = dash.window_attention(q, k, v, 4)
+    assert not out.requires_grad and asked[-1] == dict(lse=False, rest=False)
+    with torch.no_grad():
+        dash.window_attention(q.requires_grad_(True), k, v, 4)
+    assert asked[-1] == dict(lse=False, rest=False)
+    for i in range(3):
+        args = list(_qkv())
+        args[i].requires_grad_(True)
+        assert dash.window_attention(*args, 4).requires_grad
+        assert asked[-1] == dict(lse=True, rest=True)
+    args = [t.requires_grad_(True) for t in _qkv(torch.float32)]
+    dash.window_attention(*args, 4)
+    assert asked[-1] == dict(lse=True, rest=False)
