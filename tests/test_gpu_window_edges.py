@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import _window_ref as ref
-from tests.test_gpu_window import BF16, F16, _check_backward, _inputs
+from tests.test_gpu_window import BF16, F16, _check, _check_backward, _decode_inputs, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,31 @@ def test_items_of_one_step(cuda_lib, name, case):
     for _ in range(10):
         again = dash.window_bwd(q, k, v, wrong, lse, do, window, sinks)
         assert all(torch.equal(grads[n], again[n]) for n in grads)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads, kv_heads, dim, window, sinks, lens", [
+    (16, 2, 64, 0, 0, [1, 2, 3, 5, 17, 100]),
+    (32, 8, 128, 0, 0, [2, 3, 70, 4000]),
+    (16, 16, 64, 0, 0, [2, 9, 700, 3000]),
+    (32, 4, 128, 200, 10, [150, 1000, 6000]),
+])
+def test_decode_is_rounded_once(cuda_lib, heads, kv_heads, dim, window, sinks, lens, dtype):
+    """One token: the output's own rounding and the fp32 arithmetic are all of its error.  P goes into the product as
+    two values of the cache's type, u^2 of each p apart (f16: multiples of 2^-24, so at most 2^-25)."""
+    dash = cuda_lib
+    q, k, v, seqlens = _decode_inputs((heads, kv_heads, dim, dtype, window, sinks, lens), 31)
+    out = dash.window_decode(q, k, v, seqlens, window, sinks)
+    u, group = ref.ROUNDOFF[dtype], heads // kv_heads
+    for i, n in enumerate(lens):
+        j = torch.arange(n, device="cuda")
+        if window:
+            j = j[(j >= n - window) | (j < sinks)]
+        for g in range(kv_heads):
+            hs = slice(g * group, (g + 1) * group)
+            kk, vv = k[i, j, g].double(), v[i, j, g].double()
+            f = ref.forward(q[i, 0, hs].double(), kk, vv, torch.ones(group, len(j), dtype=torch.bool, device="cuda"))
+            bound = u * f["out"].abs() + (ref.moved(f, dim, dtype) + u * u)[:, None] * f["out_abs"]
+            if dtype == F16:
+                bound = bound + 2.0 ** -25 * (1 + len(j) * vv.abs().amax())
+            _check(f"out {i} {g}", out[i, 0, hs], f["out"], bound)
