@@ -33,8 +33,11 @@
 // The softmax keeps a reference m per row; while a step's sum shows no p
 // above 2^12 the row maximum is not needed.  A larger one makes the row take
 // its maximum, and O is rescaled when that moved by more than 2^8 (rare after
-// the first step).  P is rounded to the input type for the second product (the
-// tensor core's operand type); sums, m, l and O are fp32.
+// the first step).  The warp goes that way together, but only the rows whose
+// own sum asked for it move their reference: a row's bits do not depend on
+// the others of its warp, and rows behind a sequence's end, whose logits may
+// be anything, ask for nothing.  P is rounded to the input type for the second
+// product (the tensor core's operand type); sums, m, l and O are fp32.
 //
 // Bound by the chain softmax -> P V -> S of a tile, of which two are in flight
 // (tensor memory has room for two): about 1600 + 1250 clocks per 128 keys,
@@ -267,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos_a = w.pos0 + t * P, lo_b = pos_a + P - p.window;  // the tile's first position, its last row's lo
       const int pos = pos_a + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
       const int lo = pos - p.window + 1;  // first key of the row's window
-      float m_used = kNegInf, lsum = 0.f;
+      // a row behind the end starts from +inf: its p are 0 or NaN, and never call for another reference
+      float m_used = pos < w.n ? kNegInf : -kNegInf, lsum = 0.f;
       for (int i = 0; i < w.steps; ++i) {
         const int x = step + i, tok0 = w.kt.tile(i) * kStep;
         if (!(ok = warp_wait(&bars->s_full[t], x))) break;
@@ -318,17 +322,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           return s.x + s.y;
         };
         // the stores in exps are warp-wide, so the warp takes one path: the
-        // slow one when a row of it has no reference yet or left its range
-        const bool fast = __all_sync(0xffffffffu, m_used != kNegInf);
+        // second one when a row of it has no reference yet or left its range
         float corr = 1.f, lstep = 0.f;
-        if (fast) lstep = exps(-m_used);
-        if (!fast || __any_sync(0xffffffffu, !(lstep <= kMaxSum))) {
+        bool moves = m_used == kNegInf;  // this row takes its maximum
+        if (__any_sync(0xffffffffu, !moves)) {
+          lstep = exps(moves ? 0.f : -m_used);
+          moves = moves || lstep > kMaxSum;
+        }
+        if (__any_sync(0xffffffffu, moves)) {
           float mx = kNegInf;
 #pragma unroll
           for (int j = 0; j < kStep; ++j) mx = fmaxf(mx, __uint_as_float(sv[j]));
           mx *= qk_scale;
           bool resc = false;
-          if (mx != kNegInf) {
+          if (moves && mx != kNegInf) {
             if (m_used == kNegInf) {
               m_used = mx;
             } else if (mx > m_used + kRescaleLog2) {

@@ -1,6 +1,8 @@
 """GPU tests of dense / sliding-window attention at the edges between its work items, rows and number ranges (bounds of
 tests/_window_ref.py where nothing else is said)."""
 
+import math
+
 import pytest
 import torch
 
@@ -63,3 +65,41 @@ def test_decode_is_rounded_once(cuda_lib, heads, kv_heads, dim, window, sinks, l
             if dtype == F16:
                 bound = bound + 2.0 ** -25 * (1 + len(j) * vv.abs().amax())
             _check(f"out {i} {g}", out[i, 0, hs], f["out"], bound)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads, kv_heads, dim", [(4, 1, 64), (8, 1, 128), (2, 2, 64)])
+def test_what_stands_behind_the_end_moves_no_bit(cuda_lib, heads, kv_heads, dim, dtype):
+    """Rows behind a sequence's end share warps with the last rows before it.  Logits that grow along the sequence make
+    rows change their reference on the way, which must not depend on them."""
+    dash = cuda_lib
+    case = (3, 700, heads, kv_heads, dim, dtype, 500, 20, [699, 333, 401])
+    q, k, v, do, seqlens = _inputs(case, 23)
+    ramp = torch.linspace(0.2, 2.0, 700, device="cuda")[None, :, None, None]
+    q, k = (q.float() * 2).to(dtype), (k.float() * ramp).to(dtype)
+    runs = []
+    for fill in (0.0, math.nan, 1e4, -math.inf):
+        for t in (q, k, v, do):
+            for i, n in enumerate(case[-1]):
+                t[i, n:] = fill
+        rest = torch.empty_like(q)
+        out, lse = dash.window_fwd(q, k, v, 500, 20, seqlens, return_lse=True, rest=rest)
+        runs.append([out, lse, rest, *dash.window_bwd(q, k, v, out, lse, do, 500, 20, seqlens, rest=rest).values()])
+    for run in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(run, runs[0]))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_heads_move_no_bit_of_each_other(cuda_lib, dtype):
+    """Heads of a group share tiles; one with far larger logits leaves the others' bits as they are."""
+    dash = cuda_lib
+    case = (1, 900, 4, 1, 64, dtype, 600, 9, None)
+    q, k, v, _, _ = _inputs(case, 24)
+    ramp = torch.linspace(0.2, 2.0, 900, device="cuda")[None, :, None, None]
+    q, k = (q.float() * 2).to(dtype), (k.float() * ramp).to(dtype)
+    want, lse = dash.window_fwd(q, k, v, 600, 9, return_lse=True)
+    loud = q.clone()
+    loud[:, :, 2] *= 16
+    out, lse2 = dash.window_fwd(loud, k, v, 600, 9, return_lse=True)
+    for h in (0, 1, 3):
+        assert torch.equal(out[:, :, h], want[:, :, h]) and torch.equal(lse2[:, h], lse[:, h])
