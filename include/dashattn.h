@@ -470,8 +470,10 @@ dash_status_t dash_attn_window_fwd(const dash_tensor_t* q, const dash_tensor_t* 
  *   dk_j = sum_i dS_ij q_i / sqrt(d);  dv_j = sum_i p_ij dout_i
  * (dk and dv summed over the heads of the group).  No atomics: the same
  * result every time.  f16/bf16: p and dS are rounded to the input type for the
- * products (dS in dq's to twice its bits where window + sinks <= 16; f16: a dS
- * beyond 65504 overflows).
+ * products (dS in dq's to twice its bits where window + sinks <= 16, window
+ * taken as S where it is 0 or larger).  f16: both are scaled into its range
+ * for that, dS by a power of two from the largest rows of dout and of v of its
+ * sequence and KV head, so only gradients that f16 cannot hold overflow.
  *   out, rest, lse  the forward's, with the same q, k, v, seqlens, window,
  *              sinks; rest may be NULL.
  *   workspace  dash_attn_window_bwd_workspace_size() bytes, 256-byte aligned.

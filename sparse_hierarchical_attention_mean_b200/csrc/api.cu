@@ -1399,8 +1399,8 @@ void window_extent(int64_t s, int64_t* window, int64_t* sinks) {
 }
 
 struct WindowLayout {
-  size_t status, dd, nlse2, part, total;
-  int64_t n_tiles, n_chunks, chunk_tiles;
+  size_t status, dd, nlse2, part, range, total;
+  int64_t n_tiles, n_chunks, chunk_tiles, n_range;
 };
 WindowLayout window_layout(const dash_tensor_t* q, const dash_tensor_t* k, int64_t window, int64_t sinks, bool bwd) {
   WindowLayout L{};
@@ -1426,6 +1426,13 @@ WindowLayout window_layout(const dash_tensor_t* q, const dash_tensor_t* k, int64
     L.chunk_tiles = std::max<int64_t>({32, (window + 128) / pos, (far + 63) / 64});
     L.n_chunks = far > 0 ? (far + L.chunk_tiles - 1) / L.chunk_tiles : 0;
     if (L.n_chunks > 0) L.total = align256(L.part + (size_t)q->b * k->h * (L.n_chunks + 1) * 2 * 128 * q->d * 4);
+  }
+  if (q->dtype == DASH_F16) {
+    // parts of the rows of a KV head, their dout and v: 16 KB of each at least
+    const int64_t row_bytes = (q->h / k->h + 1) * q->d * 2;
+    L.n_range = std::min<int64_t>(dash::kMaxRange, (q->s * row_bytes + 16383) / 16384);
+    L.range = L.total;
+    L.total = align256(L.range + (size_t)q->b * k->h * L.n_range * 8);
   }
   return L;
 }
@@ -1513,6 +1520,8 @@ dash_status_t dash_attn_window_bwd(const dash_tensor_t* q, const dash_tensor_t* 
   p.ndd = p.dd;
   p.nlse2 = at<float>(workspace, L.nlse2);
   p.part = at<float>(workspace, L.part);
+  p.range = at<float2>(workspace, L.range);
+  p.n_range = (int)L.n_range;
   p.n_tiles = (int)L.n_tiles;
   p.n_chunks = (int)L.n_chunks;
   p.chunk_tiles = (int)L.chunk_tiles;

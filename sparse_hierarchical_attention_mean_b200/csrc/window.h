@@ -13,6 +13,7 @@ namespace dash {
 // j < sinks.  The host passes window in [1, S] (S: every key) and sinks in
 // [0, kMaxSinks], 0 when the window hides nothing.
 constexpr int kMaxSinks = 128;
+constexpr int kMaxRange = 128;  // WindowParams::n_range
 
 struct WindowParams {
   View q, k, v, out;        // [B, S, H or Hkv, D], dtype
@@ -28,6 +29,9 @@ struct WindowParams {
   // positions x G heads): [B, Hkv, n_tiles, 128]
   float* nlse2;             // -lse in log2 units; -inf on rows that are not there
   float* ndd;               // -sum_j p_ij (dout_i . v_j)
+                            // (f16: as the key kernel wants them, see the scales in window_bwd_tc.cu)
+  float2* range;            // f16: [B, Hkv, n_range] largest squared norms of rows of dout and of v
+  int n_range;
   int n_tiles;
   float* part;              // partial dk, dv of the first 128 keys [B, Hkv, n_chunks + 1, 2, 128, D]
   int n_chunks;             // items of chunk_tiles row tiles that see only sinks of the first 128 keys

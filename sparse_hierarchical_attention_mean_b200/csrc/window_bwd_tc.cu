@@ -12,7 +12,8 @@
 // dq's product takes dS as the sum of two such values (window 4: dq's error is
 // 1.5 times that of rounding dq alone without, 1.1 with; the second product
 // costs the row kernel a third of its time on long windows, nothing that shows
-// on short ones).  Everything else is fp32.  Every wait is bounded; on expiry the status word
+// on short ones).  f16 operands are scaled by powers of two into their type's
+// range (Range below).  Everything else is fp32.  Every wait is bounded; on expiry the status word
 // reads DASH_ERR_DEVICE_TIMEOUT and the roles wind down.
 #include <cuda.h>
 
@@ -29,6 +30,97 @@ constexpr int kThreads = 320;
 constexpr int kWorkers = 256;  // warps 0-7
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kTimeout = 5;  // DASH_ERR_DEVICE_TIMEOUT
+
+// ------------------------------------------------------------------ f16: the range of dS and P
+//
+// dS is as small as dout and as large as dout times v, and f16 spans 2^-24 ..
+// 2^16: a dout of 2^12 made dS overflow where the gradients can be held, one of
+// 2^-10 over 2048 keys left it 7 bits.  So dS is scaled by a power of two c per
+// sequence and KV head, undone at the end:
+//   |dS_ij| <= p_ij (|dout_i . v_j| + |D_i|) <= 2 m,  m = max |dout_i| max |v_j|
+// (D_i is a mean of dout_i . v_j), and 2^14 <= 2 m c <= 2^15, which leaves a
+// factor of two for an out with errors.  Half a step of what is below f16's
+// normal numbers is then 2^-25 / c <= 2^-38 m.  P, as an operand of dv, is at
+// most 1 and scaled by 2^10.  A kernel takes the maxima first: it reads dout
+// and v once more, 33 us of the backward's 1200 for 16K tokens of 32 / 8 heads
+// of 128 (5 TB/s), 3 of 33 for 2 x 513 of 8 / 2 heads of 64.
+template <typename T>
+constexpr bool kScaled = std::is_same<T, __half>::value;
+constexpr float kLog2P = 10.f, kScaleP = 1024.f;
+
+// What a lane of a warp read of a KV head's maxima (squared norms as bits: they
+// order like the floats, NaN above all).
+struct Range {
+  uint32_t dout, v;
+  __device__ void ask(const WindowParams& p, int b, int g, int lane) {
+    dout = v = 0u;
+    const float2* r = p.range + (int64_t)(b * p.Hkv + g) * p.n_range;
+#pragma unroll
+    for (int i = 0; i < kMaxRange; i += 32)
+      if (i + lane < p.n_range) {
+        const float2 x = r[i + lane];
+        dout = max(dout, __float_as_uint(x.x));
+        v = max(v, __float_as_uint(x.y));
+      }
+  }
+  __device__ float scale() const {
+    const float m2 = __uint_as_float(__reduce_max_sync(0xffffffffu, dout)) *
+                     __uint_as_float(__reduce_max_sync(0xffffffffu, v));
+    if (!(m2 > 0.f && m2 < -kNegInf)) return 1.f;  // all zeros, or not finite
+    const int e = (int)(__float_as_uint(m2) >> 23) - 127;  // m2 >= 2^e (it is a normal number: f16 squared twice)
+    return __uint_as_float((uint32_t)(14 - ((e + 2) >> 1) + 127) << 23);
+  }
+};
+
+constexpr int kRangeThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kRangeThreads) window_bwd_range_kernel(const WindowParams p) {
+  constexpr int kLanes = D / 8, kPass = kRangeThreads / kLanes, kAhead = 4;  // 16 bytes a lane
+  __shared__ uint32_t top[2];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int g = blockIdx.y, b = blockIdx.z, lg = __ffs(p.G) - 1;
+  const int row = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 8;
+  const int per = (p.S + gridDim.x - 1) / gridDim.x;
+  const int pos0 = min((int)blockIdx.x * per, p.S), pos1 = min(pos0 + per, window_len(p, b));
+  if (threadIdx.x < 2) top[threadIdx.x] = 0u;
+  __syncthreads();
+  auto largest = [&](const View& t, int head0, int lgh) {  // over the positions' rows of 2^lgh heads
+    const T* src = static_cast<const T*>(t.data) + (int64_t)b * t.sb + (int64_t)head0 * t.sh + col;
+    const int64_t rows = (int64_t)max(pos1 - pos0, 0) << lgh;
+    float mx = 0.f;
+    for (int64_t r0 = 0; r0 < rows; r0 += kPass * kAhead) {
+      uint4 x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t r = r0 + u * kPass + row;
+        x[u] = r < rows ? *reinterpret_cast<const uint4*>(src + (pos0 + (r >> lgh)) * t.ss +
+                                                          (r & ((1 << lgh) - 1)) * t.sh)
+                        : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float f[8], s = 0.f;
+        Elt<T>::to_float(x[u], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(f[e], f[e], s);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        // (a NaN stays: as bits it is above every number)
+        mx = __uint_as_float(max(__float_as_uint(mx), __float_as_uint(s)));
+      }
+    }
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+  };
+  const uint32_t a = largest(p.dout, g * p.G, lg), v = largest(p.v, g, 0);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&top[0], a);
+    atomicMax(&top[1], v);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    p.range[(int64_t)(b * p.Hkv + g) * p.n_range + blockIdx.x] =
+        make_float2(__uint_as_float(top[0]), __uint_as_float(top[1]));
+}
 
 // ------------------------------------------------------------------ rows: dq, D
 //
@@ -152,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the key kernel may take the SMs that are or get free; it waits for this
   // grid's end before it reads lse2 and D
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if constexpr (kScaled<T>) asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the maxima
 
   // ring tiles of an item: out (and rest), then K and V of each step
   const int n_out = p.rest.data ? 2 : 1;
@@ -288,6 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* xch = reinterpret_cast<float*>(smem + L::kOffXch) + r;
     float nlse2 = 0.f, ndd = 0.f;  // -lse2 and -D of the current item's row
     float lse_next = 0.f;          // the next item's log-sum-exp
+    [[maybe_unused]] Range range_next;
+    [[maybe_unused]] float ds_scale = 1.f;  // c of the current item; D is kept times c
     int x = 0, items = 0, step = 0;
 
     // on to the first item with steps; tiles behind the sequence's end get
@@ -314,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowItem w(p, P, it);
       const int pos = w.pos0 + (r >> lg), head = w.g * p.G + (r & (p.G - 1));
       if (pos < w.n) lse_next = p.lse[((int64_t)w.b * p.H + head) * p.S + pos];
+      if constexpr (kScaled<T>) range_next.ask(p, w.b, w.g, lane);
     };
     // lse2 and D = dout . out of an item's row: each half takes half of the
     // columns
@@ -347,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&bars->stats, lane);
       ok = warp_wait(&bars->stats, items) && ok;
       const float a = half == 0 ? mine : xch[0], b = half == 0 ? xch[kRows] : mine;
-      ndd = live ? -(a + b) : 0.f;  // the same sum in both halves
+      if constexpr (kScaled<T>) ds_scale = range_next.scale();
+      ndd = live ? -(a + b) * ds_scale : 0.f;  // the same sum in both halves
       if (threadIdx.x == 0)  // every worker has read out
         for (int y = x; y < x + n_out; ++y) tc::mbar_arrive(&bars->empty[y % kStages]);
     };
@@ -387,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo = pos - p.window + 1;
       // the warp's rows: first and last position
       const int pos_a = w.pos0 + ((q4 * 32) >> lg), pos_b = w.pos0 + ((q4 * 32 + 31) >> lg);
-      const float row_nlse2 = nlse2, row_ndd = ndd;
+      const float row_nlse2 = nlse2, row_ndd = ndd, row_scale = ds_scale;
       float2 ds_sum = make_float2(0.f, 0.f);
       for (int i = 0; i < w.steps; ++i) {
         const int y = step + i, key0 = w.kt.tile(i) * kRows + half * 64;  // the warp's keys [key0, key0 + 64)
@@ -424,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(&bars->dp_full, y))) break;
         tc::fence_after_sync();
         const float2 nd2 = make_float2(ndd, ndd);
+        [[maybe_unused]] const float2 c2 = make_float2(ds_scale, ds_scale);
         [[maybe_unused]] uint32_t low[2][16];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -442,9 +540,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const int e = c * 32 + 2 * j;
-              ds[j] = __fmul2_rn(
-                  make_float2(__uint_as_float(pf[e]), __uint_as_float(pf[e + 1])),
-                  __fadd2_rn(make_float2(__uint_as_float(dv[2 * j]), __uint_as_float(dv[2 * j + 1])), nd2));
+              const float2 dp = make_float2(__uint_as_float(dv[2 * j]), __uint_as_float(dv[2 * j + 1]));
+              ds[j] = __fmul2_rn(make_float2(__uint_as_float(pf[e]), __uint_as_float(pf[e + 1])),
+                                 kScaled<T> ? __ffma2_rn(dp, c2, nd2) : __fadd2_rn(dp, nd2));
             }
             if (!all) {
               // hidden pairs are cleared after the products: what they hold may not be finite
@@ -499,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = warp_wait(&bars->sums, item))) break;
       if (half == 0) {
         const int64_t at = ((int64_t)(w.b * p.Hkv + w.g) * p.n_tiles + w.tile) * kRows + r;
-        p.nlse2[at] = row_nlse2;
-        p.ndd[at] = pos < w.n ? row_ndd - (my_sum + *sum1) : 0.f;
+        p.nlse2[at] = row_nlse2 + (kScaled<T> ? kLog2P : 0.f);
+        p.ndd[at] = pos < w.n ? (row_ndd - (my_sum + *sum1)) * (kScaled<T> ? 1.f / kScaleP : 1.f) : 0.f;
       }
       // ---- dq of the item, each half of the workers takes half of the columns
       const bool live = pos < w.n;
@@ -516,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0u;
         }
-        if (pos < p.S) store_row32(dst + col, v, rsqrtf((float)D), p.wide);
+        if (pos < p.S) store_row32(dst + col, v, rsqrtf((float)D) / row_scale, p.wide);
       }
       tc::fence_before_sync();
       warp_arrive(&bars->dq_empty, lane);
@@ -776,6 +874,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (ItemWalk it(n_x, p.Hkv, p.B); ok && it.any(); it.next()) {
       const KeyItem w(p, lgp, it);
       const int key = w.k0 + k;
+      [[maybe_unused]] float ds_scale = 1.f;
+      if constexpr (kScaled<T>) {
+        Range range;
+        range.ask(p, w.b, w.g, lane);
+        ds_scale = range.scale();
+      }
+      // (dS is formed of P x 2^10)
+      [[maybe_unused]] const float2 c2 = make_float2(ds_scale / kScaleP, ds_scale / kScaleP);
       for (int t = w.t0; t < w.t1; ++t, ++q) {
         const int st = q % kNS, pos0 = t * P;
         const float* info = reinterpret_cast<const float*>(smem + L::kOffInfo + st * 1024) + half * 64;
@@ -864,12 +970,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; j += 4) {
             const float4 d4 = *reinterpret_cast<const float4*>(info + 128 + c * 32 + j);
             const int e = c * 32 + j;
+            auto less_d = [&](int x, float2 nd) {
+              const float2 dp = make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1]));
+              return kScaled<T> ? __ffma2_rn(dp, c2, nd) : __fadd2_rn(dp, nd);
+            };
             const float2 a = __fmul2_rn(make_float2(__uint_as_float(pf[e]), __uint_as_float(pf[e + 1])),
-                                        __fadd2_rn(make_float2(__uint_as_float(dv[j]), __uint_as_float(dv[j + 1])),
-                                                   make_float2(d4.x, d4.y)));
+                                        less_d(j, make_float2(d4.x, d4.y)));
             const float2 b = __fmul2_rn(make_float2(__uint_as_float(pf[e + 2]), __uint_as_float(pf[e + 3])),
-                                        __fadd2_rn(make_float2(__uint_as_float(dv[j + 2]), __uint_as_float(dv[j + 3])),
-                                                   make_float2(d4.z, d4.w)));
+                                        less_d(j + 2, make_float2(d4.z, d4.w)));
             dw[j >> 1] = pack2<T>(a.x, a.y);
             dw[(j >> 1) + 1] = pack2<T>(b.x, b.y);
           }
@@ -888,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         ++items;
       }
-      const float ksc = rsqrtf((float)D);
+      const float ksc = rsqrtf((float)D) / ds_scale, vsc = kScaled<T> ? 1.f / kScaleP : 1.f;
       const bool live = key < w.n;
       // each half of the workers takes half of the columns
 #pragma unroll 1
@@ -916,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(part + col + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           } else if (key < p.S) {
-            store_row32(dst + col, v, o ? 1.f : ksc, p.wide);
+            store_row32(dst + col, v, o ? vsc : ksc, p.wide);
           }
         }
       }
@@ -942,10 +1050,16 @@ __global__ void __launch_bounds__(256) window_bwd_join_kernel(const WindowParams
   const int bg = blockIdx.x, b = bg / p.Hkv, g = bg % p.Hkv;
   const int i = (blockIdx.y * 256 + threadIdx.x) * 4;  // element of [dk, dv][128][D]
   const int key = i / D % kRows, c = i % D;
-  if (key >= p.S) return;
   const float* src = p.part + (int64_t)bg * (p.n_chunks + 1) * 2 * kRows * D + i;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  float ds_scale = 1.f;
+  if constexpr (kScaled<T>) {
+    Range range;
+    range.ask(p, b, g, threadIdx.x & 31);
+    ds_scale = range.scale();
+  }
+  if (key >= p.S) return;
   for (int x = 0; x <= p.n_chunks; ++x) {
     const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)x * 2 * kRows * D);
     s.x += v.x;
@@ -955,7 +1069,7 @@ __global__ void __launch_bounds__(256) window_bwd_join_kernel(const WindowParams
   }
   const bool is_v = i >= kRows * D;
   const View& out = is_v ? p.dv : p.dk;
-  const float f = is_v ? 1.f : rsqrtf((float)D);
+  const float f = is_v ? (kScaled<T> ? 1.f / kScaleP : 1.f) : rsqrtf((float)D) / ds_scale;
   T* dst = static_cast<T*>(const_cast<void*>(out.data)) + (int64_t)b * out.sb + (int64_t)key * out.ss +
            (int64_t)g * out.sh + c;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(s.x * f, s.y * f), pack2<T>(s.z * f, s.w * f));
@@ -999,8 +1113,16 @@ cudaError_t run(const WindowParams& p, cudaStream_t stream) {
                                                : window_bwd_row_tc_kernel<T, D, false>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc)) != cudaSuccess)
       return e;
-    kern<<<(unsigned)std::min<int64_t>(row_items, p.num_sms), kThreads, L::kAlloc, stream>>>(mq, mdo, mo, mr, mk, mv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const dim3 grid((unsigned)std::min<int64_t>(row_items, p.num_sms));
+    if constexpr (kScaled<T>) {
+      window_bwd_range_kernel<T, D><<<dim3(p.n_range, p.Hkv, p.B), kRangeThreads, 0, stream>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch_early(kern, grid, kThreads, L::kAlloc, stream, mq, mdo, mo, mr, mk, mv, p);
+    } else {
+      kern<<<grid, kThreads, L::kAlloc, stream>>>(mq, mdo, mo, mr, mk, mv, p);
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
   }
   {
     using L = KeyLayout<D>;

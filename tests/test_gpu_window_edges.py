@@ -103,3 +103,65 @@ def test_heads_move_no_bit_of_each_other(cuda_lib, dtype):
     out, lse2 = dash.window_fwd(loud, k, v, 600, 9, return_lse=True)
     for h in (0, 1, 3):
         assert torch.equal(out[:, :, h], want[:, :, h]) and torch.equal(lse2[:, h], lse[:, h])
+
+
+F16_RANGES = {
+    # batch, seq, heads, kv_heads, dim, window, and the size of each sequence's incoming gradient
+    "small": (1, 2048, 4, 2, 64, 0, [2.0 ** -10]),
+    "large": (1, 600, 4, 1, 128, 4, [6200.0]),  # dS beyond 65504, the gradients below it
+    "large, window": (1, 600, 2, 2, 64, 40, [2.0 ** 13]),
+    "one small beside one large": (2, 700, 4, 2, 64, 0, [2.0 ** 8, 2.0 ** -8]),
+    "zero beside ones": (2, 300, 2, 1, 64, 0, [0.0, 1.0]),
+}
+
+
+@pytest.mark.parametrize("name", list(F16_RANGES))
+def test_gradients_over_the_range_of_f16(cuda_lib, name):
+    """dS as an f16 operand neither overflows nor loses its low bits where the gradients themselves can be held.
+
+    dS is scaled by a power of two c, 2^15 / (2 m) >= c > 2^13 / (2 m) with m the product of the largest norms of a
+    row of dout and of v, and lies on multiples of 2^-24: half a step is 2^-25 / c < 2^-37 m.  P is scaled by 2^10."""
+    dash = cuda_lib
+    b, s, h, hkv, d, window, sizes = F16_RANGES[name]
+    case = (b, s, h, hkv, d, F16, window, 0, None)
+    q, k, v, do, _ = _inputs(case, 25)
+    do = (do.float() * torch.tensor(sizes, device="cuda")[:, None, None, None]).half()
+    rest = torch.empty_like(q)
+    out, lse = dash.window_fwd(q, k, v, window, return_lse=True, rest=rest)
+    grads = dash.window_bwd(q, k, v, out, lse, do, window, rest=rest)
+    seen, group = ref.visible(s, window, 0, q.device), h // hkv
+    for i in range(b):
+        for g in range(hkv):
+            kk, vv, tot, rel = k[i, :, g].double(), v[i, :, g].double(), {}, 0.0
+            heads = range(g * group, (g + 1) * group)
+            m = float(max(do[i, :, x].double().norm(dim=-1).max() for x in heads) * vv.norm(dim=-1).max())
+            for hh in heads:
+                f = ref.forward(q[i, :, hh].double(), kk, vv, seen)
+                exact_out = out[i, :, hh].double() + rest[i, :, hh].double()
+                one = ref.backward(q[i, :, hh].double(), kk, vv, exact_out, do[i, :, hh].double(), f)
+                for x in ("dq_sub", "dk_sub"):
+                    one[x] = one[x] * 2.0 ** -12 * m  # the reference's are those of half a step of 2^-25
+                one["dv_sub"] = one["dv_sub"] * 2.0 ** -10
+                r = float(ref.moved(f, d, F16).max()) * 2
+                rel = max(rel, r)
+                _check(f"dq {i} {hh}", grads["dq"][i, :, hh], one["dq"],
+                       ref.grad_bound(one, "dq", r, F16, d, 0 < window <= 16))
+                for key, x in one.items():
+                    if key[:2] in ("dk", "dv"):
+                        tot[key] = tot[key] + x if key in tot else x
+            for n in ("dk", "dv"):
+                _check(f"{n} {i} {g}", grads[n][i, :, g], tot[n], ref.grad_bound(tot, n, rel, F16, d))
+
+
+def test_sequences_of_a_batch_stay_apart(cuda_lib):
+    """A sequence's gradients are the same bits whatever the others of its batch hold."""
+    dash = cuda_lib
+    case = (3, 400, 4, 2, 64, F16, 100, 4, None)
+    q, k, v, do, _ = _inputs(case, 26)
+    out, lse = dash.window_fwd(q, k, v, 100, 4, return_lse=True)
+    want = dash.window_bwd(q, k, v, out, lse, do, 100, 4)
+    do[0] *= 2.0 ** 9
+    do[2] = 0
+    got = dash.window_bwd(q, k, v, out, lse, do, 100, 4)
+    assert all(torch.equal(got[n][1], want[n][1]) for n in want)
+    assert all((got[n][2] == 0).all() for n in got)
