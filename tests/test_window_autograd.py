@@ -1,4 +1,4 @@
-"""The differentiable form of sliding-window attention around its kernels, which a stand-in takes the place of (no GPU)."""
+"""The differentiable form of sliding-window attention around its kernels, which a stand-in replaces (no GPU)."""
 
 import pytest
 import torch
