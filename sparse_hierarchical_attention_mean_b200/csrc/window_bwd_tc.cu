@@ -8,8 +8,9 @@
 // does not depend on timing; S and dP are computed in both (7 products
 // instead of 5).  Tiles of rows are 128 = (128 / G positions) x (G heads).
 // p and dS are rounded to the input type as operands of the second products;
-// where a row sees at most kFewKeys keys, whose roundings hardly average out,
-// dq's product takes dS as the sum of two such values (window 4: dq's error is
+// where the call's window and sinks are at most kFewKeys keys, whose roundings
+// hardly average out, dq's product takes dS as the sum of two such values (the
+// first rows of other calls see as few and do without; window 4: dq's error is
 // 1.5 times that of rounding dq alone without, 1.1 with; the second product
 // costs the row kernel a third of its time on long windows, nothing that shows
 // on short ones).  f16 operands are scaled by powers of two into their type's
