@@ -68,6 +68,30 @@ def test_decode_is_rounded_once(cuda_lib, heads, kv_heads, dim, window, sinks, l
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads, kv_heads, dim", [(8, 1, 128), (4, 4, 64), (6, 3, 64)])
+def test_decode_of_growing_logits(cuda_lib, heads, kv_heads, dim, dtype):
+    """One token whose logits grow along the cache by hundreds, so that the reference moves again and again and takes
+    both parts of the sum with it: the bound of one rounding."""
+    dash = cuda_lib
+    lens = [900, 333, 3000]
+    q, k, v, seqlens = _decode_inputs((heads, kv_heads, dim, dtype, 0, 0, lens), 32)
+    ramp = torch.linspace(0.1, 3.0, k.shape[1], device="cuda")[None, :, None, None]
+    q, k = (q.float() * 6).to(dtype), (k.float() * ramp).to(dtype)
+    out, lse = dash.window_decode(q, k, v, seqlens, return_lse=True)
+    u, group = ref.ROUNDOFF[dtype], heads // kv_heads
+    for i, n in enumerate(lens):
+        for g in range(kv_heads):
+            hs = slice(g * group, (g + 1) * group)
+            kk, vv = k[i, :n, g].double(), v[i, :n, g].double()
+            f = ref.forward(q[i, 0, hs].double(), kk, vv, torch.ones(group, n, dtype=torch.bool, device="cuda"))
+            bound = u * f["out"].abs() + (ref.moved(f, dim, dtype) + u * u)[:, None] * f["out_abs"]
+            if dtype == F16:
+                bound = bound + 2.0 ** -25 * (1 + n * vv.abs().amax())
+            _check(f"out {i} {g}", out[i, 0, hs], f["out"], bound)
+            _check(f"lse {i} {g}", lse[i, hs], f["lse"], ref.lse_bound(f, dim, dtype))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("heads, kv_heads, dim", [(4, 1, 64), (8, 1, 128), (2, 2, 64)])
 def test_what_stands_behind_the_end_moves_no_bit(cuda_lib, heads, kv_heads, dim, dtype):
     """Rows behind a sequence's end share warps with the last rows before it.  Logits that grow along the sequence make
@@ -165,3 +189,27 @@ def test_sequences_of_a_batch_stay_apart(cuda_lib):
     got = dash.window_bwd(q, k, v, out, lse, do, 100, 4)
     assert all(torch.equal(got[n][1], want[n][1]) for n in want)
     assert all((got[n][2] == 0).all() for n in got)
+
+
+def test_f16_scales_follow_a_replay(cuda_lib):
+    """The scale of dS belongs to the values that a captured backward meets when it is replayed, on whatever stream."""
+    dash = cuda_lib
+    case = (2, 500, 4, 2, 64, F16, 90, 4, [500, 123])
+    q, k, v, do, seqlens = _inputs(case, 27)
+    out, lse = dash.window_fwd(q, k, v, 90, 4, seqlens, return_lse=True)
+    dash.window_bwd(q, k, v, out, lse, do, 90, 4, seqlens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grads = dash.window_bwd(q, k, v, out, lse, do, 90, 4, seqlens)
+    first = do.clone()
+    side = torch.cuda.Stream()
+    for size in (2.0 ** -9, 2.0 ** 10, 1.0):
+        do.copy_(first * size)
+        want = dash.window_bwd(q, k, v, out, lse, do, 90, 4, seqlens)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        other = dash.window_bwd(q, k, v, out, lse, do, 90, 4, seqlens)  # beside the replay, in its own workspace
+        torch.cuda.synchronize()
+        assert all(torch.equal(grads[n], want[n]) and torch.equal(other[n], want[n]) for n in want)
